@@ -238,6 +238,96 @@ macaq_status macaq_act_quant_gather(const void *X, int64_t x_rows, const int32_t
 macaq_status macaq_moe_combine(const void *Y, int64_t y_rows, int64_t N, const int32_t *pos, const float *weights,
                                int64_t T, int32_t topk, void *out, int32_t out_dtype, macaq_stream_t stream);
 
+/* How moe_route turns a chosen logit into a weight. */
+typedef enum { MACAQ_SCORE_SOFTMAX = 0, MACAQ_SCORE_SIGMOID = 1 } macaq_scoring;
+
+/*
+ * The router of a mixture-of-experts layer: top-k experts, their weights, and the row plan that
+ * macaq_act_quant_gather, macaq_grouped_linear, macaq_moe_combine and macaq_moe_w4a16 take.
+ *   logits        device [T, E], bf16 or fp32 per in_dtype (MACAQ_OUT_BF16 / MACAQ_OUT_F32), row t at
+ *                 logits + t * ld elements (ld >= E), aligned to its element. -inf or NaN masks the
+ *                 expert for that token; +inf counts as the largest finite fp32.
+ *   topk          1 <= topk <= min(E, 32): the experts of largest logit, ties to the lowest expert, in
+ *                 falling order. A choice that falls on a masked expert is dropped: id -1, weight 0, pos -1.
+ *   scoring       softmax: p = softmax of the token's unmasked logits; sigmoid: p = 1 / (1 + exp(-logit))
+ *   renormalize   nonzero: weight = scale * p / (sum of p over the token's choices); 0: scale * p
+ *   weights       device fp32 [T, topk] (written), ids device int32 [T, topk] (written)
+ *   group_offsets, row_index, pos: the plan of macaq_row_groups(ids) (written)
+ *   1 <= E <= 1024, T >= 0 (T == 0 writes zero offsets), T * topk < 2^30. fp32 arithmetic throughout.
+ */
+macaq_status macaq_moe_route(const void *logits, int32_t in_dtype, int64_t ld, int64_t T, int32_t E, int32_t topk,
+                             int32_t scoring, int32_t renormalize, float scale, float *weights, int32_t *ids,
+                             int32_t *group_offsets, int32_t *row_index, int32_t *pos, macaq_stream_t stream);
+
+/*
+ * Rows sorted by group (expert or adapter): a stable counting sort of the R = T * topk entries of ids.
+ *   ids            device int32 [T, topk]; an id outside [0, E) belongs to no group. An id may repeat
+ *                  within a token.
+ *   group_offsets  device int32 [E + 1] (written): rows [group_offsets[g], group_offsets[g + 1]) are group
+ *                  g's, in the order of their entries; group_offsets[E] is the number of grouped rows
+ *   row_index      device int32 [R] (written): the token (entry / topk) of every sorted row; the entries
+ *                  of no group follow the last group, in their order
+ *   pos            device int32 [R] (written): the sorted row of every entry, -1 for those of no group
+ *   1 <= E <= 1024, topk >= 1, T >= 0, T * topk < 2^30. ids, weights and row plans are 16-byte aligned.
+ */
+macaq_status macaq_row_groups(const int32_t *ids, int64_t T, int32_t topk, int32_t E, int32_t *group_offsets,
+                              int32_t *row_index, int32_t *pos, macaq_stream_t stream);
+
+/*
+ * A whole mixture-of-experts layer for few tokens (decode), in the weight-only mode: MXFP4 weights,
+ * bf16 activations, two launches.
+ *     x' = X[t] diag(inv_s_gu[e]) H_b;   G, U = x' dq(W'_gu[e])^T  (64-row interleaved, as macaq_linear_swiglu)
+ *     h' = (silu(G) U) diag(inv_s_down[e]) H_b';   y_r = h' dq(W'_down[e])^T
+ *     out[t] = bf16( sum over j of weights[t, j] * y_{pos[t, j]} ),  fp32 accumulation
+ *   X              device bf16 [T, K], 0 <= T <= 64 (T == 0: no-op; larger: MACAQ_ERR_SHAPE)
+ *   weights, group_offsets, row_index, pos: from macaq_moe_route (or any plan with
+ *                  row_index[pos[t, j]] == t and each sorted row named by at most one pos; pos outside
+ *                  [0, group_offsets[E]) is a dropped choice). Read on the device; values out of range
+ *                  are clamped or skipped, so no access leaves the buffers.
+ *   topk, E        1 <= topk <= 32, 1 <= E <= 1024
+ *   Wq_gu, Wsf_gu  u8 [E, 2I, K/2] and [E, macaq_sf_bytes(2I, K)]; Wq_down, Wsf_down  u8 [E, N, I/2] and
+ *                  [E, macaq_sf_bytes(N, I)] (macaq_prep_weights per expert). Scale bytes up to 252.
+ *   inv_s_gu       device fp32 [E, K] or NULL (1); inv_s_down device fp32 [E, I] or NULL
+ *   had_block      of the gate/up input, had_block_down of the down input, each in {1, 16, 32, 64, 128}
+ *   out            device bf16 [T, N] (written; a token whose choices are all dropped gets zeros)
+ *   workspace      at least macaq_moe_w4a16_workspace_bytes(T, topk, E, K, I, N) bytes; no initial value needed,
+ *                  nothing kept between calls. Calls that may overlap need separate workspaces.
+ *   K, I, N multiples of 128; K, I <= 16384; N <= 2^20.
+ * Sources: glonce.com page, paragraph 3 (weight-only mode) and paragraph 5 (grouped matmul); aipolix.com page,
+ * paragraph 2 (the transform at the input of every linear).
+ */
+size_t macaq_moe_w4a16_workspace_bytes(int64_t T, int32_t topk, int32_t E, int64_t K, int64_t I, int64_t N);
+macaq_status macaq_moe_w4a16(const void *X, int64_t T, int64_t K, const float *weights, int32_t topk,
+                             const int32_t *group_offsets, int32_t E, const int32_t *row_index, const int32_t *pos,
+                             const uint8_t *Wq_gu, const uint8_t *Wsf_gu, const float *inv_s_gu, int32_t had_block, int64_t I,
+                             const uint8_t *Wq_down, const uint8_t *Wsf_down, const float *inv_s_down,
+                             int32_t had_block_down, int64_t N, void *out, void *workspace, size_t ws_bytes,
+                             macaq_stream_t stream);
+
+/*
+ * Low-rank adapters of many requests beside a shared projection:
+ *     out[m] = Y[m] + scale[a] * (X[m] A[a]^T) B[a]^T      for the rows m of adapter a
+ * with X A^T and the sum in fp32, rounded once to out's type. Y is the projection's output, from any of the
+ * linear calls; X its input (before the activation transform).
+ *   Y, out         device [M, N], bf16 or fp32 per dtype (MACAQ_OUT_BF16 / MACAQ_OUT_F32), rows ldy and ldo
+ *                  elements apart (>= N): a column slice of a fused projection is fine. out == Y (with
+ *                  ldo == ldy) updates in place and leaves the rows of no adapter untouched; otherwise the
+ *                  buffers must not overlap and those rows are copied.
+ *   X              device bf16 [M, K], rows ldx elements apart (>= K)
+ *   A, B           device bf16 [L, r, K] and [L, N, r]
+ *   scale          device fp32 [L] or NULL (1)
+ *   group_offsets  device int32 [L + 1], row_index device int32 [M]: a row plan of the M rows by adapter
+ *                  (macaq_row_groups with topk = 1). row_index lists every row once: a row listed twice
+ *                  gets one of the two results. NULL row_index: the rows are sorted already. Read on the
+ *                  device; out-of-range values are clamped or skipped.
+ *   K, N, r, ldx, ldy, ldo multiples of 8 (ldy, ldo of fp32: 4); 8 <= r <= 128; 1 <= L <= 1024; M >= 0
+ *   (0: no-op); M, K, N < 2^31. Every pointer 16-byte aligned, scale 4-byte.
+ */
+macaq_status macaq_lora_add(const void *Y, int64_t ldy, void *out, int64_t ldo, int32_t dtype, const void *X, int64_t ldx,
+                            int64_t M, int64_t K, int64_t N, const void *A, const void *B, int32_t r, int32_t L,
+                            const float *scale, const int32_t *group_offsets, const int32_t *row_index,
+                            macaq_stream_t stream);
+
 /*
  * Dense W4A4 linear: Y[m, n] = sum_k dq(A[m, k]) * dq(W'[n, k]), fp32 accumulation on the tcgen05
  * tensor cores (kind::mxf4 block-scaled MMA), written as bf16 (round-to-nearest-even) or fp32.

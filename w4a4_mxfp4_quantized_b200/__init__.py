@@ -27,6 +27,7 @@ __all__ = [
     "prep_weights", "act_quant", "linear", "linear_fixed_scratch", "grouped_linear", "device_status",
     "set_wait_limit_ns", "check_group_offsets", "act_quant_gather", "moe_combine",
     "linear_swiglu", "swiglu_act_quant", "interleave_gate_up", "flip_refine", "act_transform", "linear_w4a16",
+    "SCORE_SOFTMAX", "SCORE_SIGMOID", "moe_route", "row_groups", "moe_w4a16", "moe_w4a16_workspace_bytes", "lora_add",
     "library_path", "lib",
 ]
 
@@ -38,11 +39,13 @@ _lib = None
 OUT_BF16, OUT_F32 = 0, 1
 WORKSPACE_COUNTER_BYTES = 65536  # MACAQ_WORKSPACE_COUNTER_BYTES: the zero-between-calls counter region
 A_QUANTIZED, A_BF16_FUSED, A_BF16_ONE_LAUNCH = 0, 1, 2
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _i32 = ctypes.c_int32
 _sz = ctypes.c_size_t
+_f32 = ctypes.c_float
 
 _SIGNATURES = {
     "macaq_status_str": ([ctypes.c_int], ctypes.c_char_p),
@@ -71,6 +74,13 @@ _SIGNATURES = {
     "macaq_act_transform": ([_vp, _vp, _i64, _i64, _i32, _vp, _vp], ctypes.c_int),
     "macaq_linear_w4a16_workspace_bytes": ([_i64, _i64, _i64], _sz),
     "macaq_linear_w4a16": ([_vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _i32, _vp, _sz, _vp], ctypes.c_int),
+    "macaq_moe_route": ([_vp, _i32, _i64, _i64, _i32, _i32, _i32, _i32, _f32, _vp, _vp, _vp, _vp, _vp, _vp], ctypes.c_int),
+    "macaq_row_groups": ([_vp, _i64, _i32, _i32, _vp, _vp, _vp, _vp], ctypes.c_int),
+    "macaq_moe_w4a16_workspace_bytes": ([_i64, _i32, _i32, _i64, _i64, _i64], _sz),
+    "macaq_moe_w4a16": ([_vp, _i64, _i64, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _vp, _vp, _vp, _i32,
+                         _i64, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "macaq_lora_add": ([_vp, _i64, _vp, _i64, _i32, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp],
+                       ctypes.c_int),
 }
 
 
@@ -311,6 +321,142 @@ def linear_w4a16(X: torch.Tensor, inv_s: torch.Tensor | None, Wq: torch.Tensor, 
         _ptr(X), _ptr(inv_s), M, N, K, had_block, _ptr(Wq), _ptr(Wsf), _ptr(Y), out_dtype, _ptr(workspace), ws_bytes,
         _stream(dev)))
     return Y
+
+
+def _arg(name: str, t: torch.Tensor, dtype, shape, dev) -> int:
+    """The pointer of a contiguous CUDA tensor on `dev` of the given type and shape (ValueError otherwise)."""
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _cuda(name: str, t: torch.Tensor) -> torch.device:
+    if not t.is_cuda:
+        raise ValueError(f"{name}: libmacaq takes CUDA tensors")
+    return t.device
+
+
+def _call(fn: str, dev: torch.device, *args) -> None:
+    """Calls a library function on the tensors' device (made current for the call) and its current stream."""
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _call(fn, dev, *args)
+    _check(fn, getattr(lib(), fn)(*args, _stream(dev)))
+
+
+_ROWS_DTYPE = {torch.bfloat16: OUT_BF16, torch.float32: OUT_F32}
+
+
+def _plan_out(T: int, topk: int, E: int, dev, group_offsets, row_index, pos, pos_shape):
+    i32 = torch.int32
+    group_offsets = torch.empty(E + 1, dtype=i32, device=dev) if group_offsets is None else group_offsets
+    row_index = torch.empty(T * topk, dtype=i32, device=dev) if row_index is None else row_index
+    pos = torch.empty(pos_shape, dtype=i32, device=dev) if pos is None else pos
+    ptrs = (_arg("group_offsets", group_offsets, i32, (E + 1,), dev), _arg("row_index", row_index, i32, (T * topk,), dev),
+            _arg("pos", pos, i32, pos_shape, dev))
+    return (group_offsets, row_index, pos), ptrs
+
+
+def moe_route(logits: torch.Tensor, topk: int, *, scoring: int = SCORE_SOFTMAX, renormalize: bool = True, scale: float = 1.0,
+              weights=None, ids=None, group_offsets=None, row_index=None, pos=None):
+    """Router of a mixture-of-experts layer: the topk experts of every token and the row plan by expert.
+
+    logits: bf16 or fp32 CUDA [T, E] (rows may be strided); -inf or NaN masks an expert. Returns (weights fp32 [T, topk],
+    ids int32 [T, topk], group_offsets int32 [E + 1], row_index int32 [T * topk], pos int32 [T, topk]): row_index and
+    group_offsets go to act_quant_gather and grouped_linear, pos and weights to moe_combine, all four to moe_w4a16.
+    Choices that fall on masked experts are dropped (id -1, weight 0, pos -1)."""
+    dev = _cuda("logits", logits)
+    if logits.dim() != 2 or logits.dtype not in _ROWS_DTYPE or (logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise ValueError("logits: expected a bf16 or fp32 tensor [T, E] with contiguous rows")
+    T, E = logits.shape
+    ld = logits.stride(0) if T > 1 else E
+    weights = torch.empty(T, topk, dtype=torch.float32, device=dev) if weights is None else weights
+    ids = torch.empty(T, topk, dtype=torch.int32, device=dev) if ids is None else ids
+    plan, ptrs = _plan_out(T, topk, E, dev, group_offsets, row_index, pos, (T, topk))
+    _call("macaq_moe_route", dev, logits.data_ptr(), _ROWS_DTYPE[logits.dtype], ld, T, E, topk, scoring, int(renormalize),
+          scale, _arg("weights", weights, torch.float32, (T, topk), dev), _arg("ids", ids, torch.int32, (T, topk), dev), *ptrs)
+    return (weights, ids, *plan)
+
+
+def row_groups(ids: torch.Tensor, E: int, *, group_offsets=None, row_index=None, pos=None):
+    """Rows sorted by group (expert or adapter): ids int32 CUDA [T] or [T, topk], values outside [0, E) in no group.
+    Returns (group_offsets int32 [E + 1], row_index int32 [T * topk], pos int32, ids' shape)."""
+    dev = _cuda("ids", ids)
+    if ids.dim() not in (1, 2):
+        raise ValueError("ids: expected [T] or [T, topk]")
+    T, topk = ids.shape[0], (ids.shape[1] if ids.dim() == 2 else 1)
+    plan, ptrs = _plan_out(T, topk, E, dev, group_offsets, row_index, pos, ids.shape)
+    _call("macaq_row_groups", dev, _arg("ids", ids, torch.int32, ids.shape, dev), T, topk, E, *ptrs)
+    return plan
+
+
+def moe_w4a16_workspace_bytes(T: int, topk: int, E: int, K: int, I: int, N: int) -> int:
+    return int(lib().macaq_moe_w4a16_workspace_bytes(T, topk, E, K, I, N))
+
+
+def moe_w4a16(X: torch.Tensor, weights: torch.Tensor, group_offsets: torch.Tensor, row_index: torch.Tensor,
+              pos: torch.Tensor, Wq_gu: torch.Tensor, Wsf_gu: torch.Tensor, Wq_down: torch.Tensor, Wsf_down: torch.Tensor, *,
+              inv_s_gu: torch.Tensor | None = None, inv_s_down: torch.Tensor | None = None, had_block: int = 32,
+              had_block_down: int = 32, out=None, workspace=None):
+    """A whole expert layer for few tokens (T <= 64) on MXFP4 weights and bf16 activations: gate/up, SwiGLU, down and the
+    weighted sum of each token's choices. X bf16 [T, K]; weights, group_offsets, row_index and pos from moe_route;
+    Wq_gu [E, 2I, K/2] (interleave_gate_up, then prep_weights), Wq_down [E, N, I/2], their tiled scales
+    [E, sf_bytes]; inv_s_gu [E, K], inv_s_down [E, I] or None. Returns out bf16 [T, N]."""
+    dev = _cuda("X", X)
+    u8, i32, f32 = torch.uint8, torch.int32, torch.float32
+    if X.dim() != 2 or pos.dim() != 2 or Wq_gu.dim() != 3 or Wq_down.dim() != 3:
+        raise ValueError("moe_w4a16 takes X [T, K], pos [T, topk], Wq_gu [E, 2I, K/2] and Wq_down [E, N, I/2]")
+    T, K = X.shape
+    topk = pos.shape[1]
+    E, N = Wq_gu.shape[0], Wq_down.shape[1]
+    I = Wq_gu.shape[1] // 2
+    out = torch.empty(T, N, dtype=torch.bfloat16, device=dev) if out is None else out
+    if workspace is None:   # of this call alone: calls on other streams and captured graphs have their own
+        workspace = torch.empty(max(moe_w4a16_workspace_bytes(T, topk, E, K, I, N), 16), dtype=u8, device=dev)
+    _call("macaq_moe_w4a16", dev, _arg("X", X, torch.bfloat16, (T, K), dev), T, K,
+          _arg("weights", weights, f32, (T, topk), dev), topk, _arg("group_offsets", group_offsets, i32, (E + 1,), dev), E,
+          _arg("row_index", row_index, i32, (T * topk,), dev), _arg("pos", pos, i32, (T, topk), dev),
+          _arg("Wq_gu", Wq_gu, u8, (E, 2 * I, K // 2), dev), _arg("Wsf_gu", Wsf_gu, u8, (E, 2 * I * (K // 32)), dev),
+          None if inv_s_gu is None else _arg("inv_s_gu", inv_s_gu, f32, (E, K), dev), had_block, I,
+          _arg("Wq_down", Wq_down, u8, (E, N, I // 2), dev), _arg("Wsf_down", Wsf_down, u8, (E, N * (I // 32)), dev),
+          None if inv_s_down is None else _arg("inv_s_down", inv_s_down, f32, (E, I), dev), had_block_down, N,
+          _arg("out", out, torch.bfloat16, (T, N), dev), _arg("workspace", workspace, u8, workspace.shape, dev),
+          workspace.numel())
+    return out
+
+
+def _rows(name: str, t: torch.Tensor, dtype, M: int, N: int, dev):
+    """Pointer and row stride of a [M, N] tensor whose rows are contiguous."""
+    if t.dtype is not dtype or t.shape != (M, N) or t.device != dev or (N > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: expected a {dtype} tensor of shape {(M, N)} with contiguous rows on {dev}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr(), (t.stride(0) if M > 1 else N)
+
+
+def lora_add(Y: torch.Tensor, X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, group_offsets: torch.Tensor,
+             row_index: torch.Tensor | None = None, *, scale: torch.Tensor | None = None, out=None):
+    """Low-rank adapters of many requests beside a shared projection: out[m] = Y[m] + scale[a] (X[m] A[a]^T) B[a]^T for the
+    rows m of adapter a. Y bf16 or fp32 [M, N] (a column slice is fine), the output of any of the linear calls on X
+    bf16 [M, K]; A bf16 [L, r, K], B bf16 [L, N, r], scale fp32 [L] or None. The rows of every adapter:
+    group_offsets and row_index from row_groups(adapter of each row, L); row_index None when the rows are sorted.
+    out None updates Y in place."""
+    dev = _cuda("Y", Y)
+    if Y.dim() != 2 or X.dim() != 2 or A.dim() != 3 or Y.dtype not in _ROWS_DTYPE:
+        raise ValueError("lora_add takes Y [M, N] in bf16 or fp32, X [M, K], A [L, r, K] and B [L, N, r]")
+    M, N = Y.shape
+    L, r, K = A.shape
+    out = Y if out is None else out
+    yp, ldy = _rows("Y", Y, Y.dtype, M, N, dev)
+    op, ldo = _rows("out", out, Y.dtype, M, N, dev)
+    xp, ldx = _rows("X", X, torch.bfloat16, M, K, dev)
+    bf16, i32 = torch.bfloat16, torch.int32
+    _call("macaq_lora_add", dev, yp, ldy, op, ldo, _ROWS_DTYPE[Y.dtype], xp, ldx, M, K, N,
+          _arg("A", A, bf16, (L, r, K), dev), _arg("B", B, bf16, (L, N, r), dev), r, L,
+          None if scale is None else _arg("scale", scale, torch.float32, (L,), dev),
+          _arg("group_offsets", group_offsets, i32, (L + 1,), dev),
+          None if row_index is None else _arg("row_index", row_index, i32, (M,), dev))
+    return out
 
 
 def _out(M, N, out_dtype, dev, Y):

@@ -18,8 +18,11 @@
 #include "macaq.h"
 #include "flip.cuh"
 #include "gemm.cuh"
+#include "lora.cuh"
 #include "moe.cuh"
+#include "moe_w4a16.cuh"
 #include "quant.cuh"
+#include "route.cuh"
 #include "w4a16.cuh"
 
 namespace macaq {
@@ -1029,6 +1032,151 @@ macaq_status moe_combine(const void *Y, int64_t y_rows, int64_t N, const int32_t
     return launch(moe_combine_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kCombineThreads), 0, st, 1, c);
 }
 
+// ------------------------------------------------------------------------ router and row plan
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Shapes of a row plan shared by the router, the row sort and their users.
+bool plan_shape_ok(int64_t T, int32_t topk, int32_t E) {
+    return T >= 0 && topk >= 1 && E >= 1 && E <= kRouteMaxExperts && T <= ((int64_t(1) << 30) - 1) / topk;
+}
+
+macaq_status run_row_groups(const GroupArgs &g, cudaStream_t st) {
+    const size_t smem = (kGroupThreads / 32 + 1) * static_cast<size_t>(g.E + 1) * sizeof(int32_t);
+    macaq_status s = set_smem(row_groups_kernel, smem);
+    if (s != MACAQ_OK) return s;
+    return launch(row_groups_kernel, dim3(1), dim3(kGroupThreads), smem, st, 1, g);
+}
+
+macaq_status row_groups(const int32_t *ids, int64_t T, int32_t topk, int32_t E, int32_t *offsets, int32_t *row_index,
+                        int32_t *pos, cudaStream_t st) {
+    if (!plan_shape_ok(T, topk, E)) return MACAQ_ERR_SHAPE;
+    if (offsets == nullptr || (T > 0 && (ids == nullptr || row_index == nullptr || pos == nullptr))) return MACAQ_ERR_INVALID_ARG;
+    if (!aligned16(ids) || !aligned16(offsets) || !aligned16(row_index) || !aligned16(pos)) return MACAQ_ERR_ALIGNMENT;
+    DeviceInfo dev;
+    macaq_status s = device_info(&dev);
+    if (s != MACAQ_OK) return s;
+    GroupArgs g;
+    g.ids = ids;
+    g.R = T * topk;
+    g.topk = topk;
+    g.E = E;
+    g.offsets = offsets;
+    g.row_index = row_index;
+    g.pos = pos;
+    return run_row_groups(g, st);
+}
+
+template <int kVpl>
+macaq_status run_route_topk(const RouteArgs &a, unsigned blocks, cudaStream_t st) {
+    return launch(route_topk_kernel<kVpl>, dim3(blocks), dim3(kRouteWarps * 32), 0, st, 1, a);
+}
+
+macaq_status moe_route(const void *logits, int32_t in_dtype, int64_t ld, int64_t T, int32_t E, int32_t topk, int32_t scoring,
+                       int32_t renorm, float scale, float *weights, int32_t *ids, int32_t *offsets, int32_t *row_index,
+                       int32_t *pos, cudaStream_t st) {
+    if (!plan_shape_ok(T, topk, E) || topk > kRouteMaxTopk || topk > E || ld < E || ld >= (int64_t(1) << 31))
+        return MACAQ_ERR_SHAPE;
+    if ((in_dtype != MACAQ_OUT_BF16 && in_dtype != MACAQ_OUT_F32) ||
+        (scoring != MACAQ_SCORE_SOFTMAX && scoring != MACAQ_SCORE_SIGMOID))
+        return MACAQ_ERR_INVALID_ARG;
+    if (offsets == nullptr || (T > 0 && (logits == nullptr || weights == nullptr || ids == nullptr || row_index == nullptr ||
+                                         pos == nullptr)))
+        return MACAQ_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(logits) & (in_dtype == MACAQ_OUT_F32 ? 3u : 1u)) || !aligned16(weights) ||
+        !aligned16(ids) || !aligned16(offsets) || !aligned16(row_index) || !aligned16(pos))
+        return MACAQ_ERR_ALIGNMENT;
+    DeviceInfo dev;
+    macaq_status s = device_info(&dev);
+    if (s != MACAQ_OK) return s;
+    if (T > 0) {
+        RouteArgs a;
+        a.logits = logits;
+        a.ld = ld;
+        a.T = T;
+        a.E = E;
+        a.topk = topk;
+        a.f32 = in_dtype == MACAQ_OUT_F32;
+        a.sigmoid = scoring == MACAQ_SCORE_SIGMOID;
+        a.renorm = renorm != 0;
+        a.scale = scale;
+        a.weights = weights;
+        a.ids = ids;
+        const int64_t want = (T + kRouteWarps - 1) / kRouteWarps;
+        const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(want, static_cast<int64_t>(dev.sms) * 8));
+        if (E <= 32) s = run_route_topk<1>(a, blocks, st);
+        else if (E <= 64) s = run_route_topk<2>(a, blocks, st);
+        else if (E <= 128) s = run_route_topk<4>(a, blocks, st);
+        else if (E <= 256) s = run_route_topk<8>(a, blocks, st);
+        else if (E <= 512) s = run_route_topk<16>(a, blocks, st);
+        else s = run_route_topk<32>(a, blocks, st);
+        if (s != MACAQ_OK) return s;
+    }
+    return row_groups(ids, T, topk, E, offsets, row_index, pos, st);
+}
+
+// ------------------------------------------------------------------------ few-token expert layer
+size_t moe_w4a16_ws(int64_t T, int32_t topk, int64_t I) {
+    return static_cast<size_t>(T) * topk * static_cast<size_t>(I) * sizeof(float);
+}
+
+bool moe_w4a16_shape_ok(int64_t T, int32_t topk, int32_t E, int64_t K, int64_t I, int64_t N) {
+    return T >= 0 && T <= kMoeMaxT && topk >= 1 && topk <= kRouteMaxTopk && E >= 1 && E <= kRouteMaxExperts && K > 0 &&
+           K % 128 == 0 && K <= 16384 && I > 0 && I % 128 == 0 && I <= 16384 && N > 0 && N % 128 == 0 &&
+           N <= (int64_t(1) << 20);
+}
+
+macaq_status moe_w4a16(const MoeArgs &a, void *workspace, size_t ws_bytes, cudaStream_t st) {
+    if (!moe_w4a16_shape_ok(a.T, a.topk, a.E, a.K, a.I, a.N)) return MACAQ_ERR_SHAPE;
+    if (!valid_block(a.b_gu) || !valid_block(a.b_dn)) return MACAQ_ERR_UNSUPPORTED;
+    if (a.T == 0) return MACAQ_OK;
+    if (a.x == nullptr || a.weights == nullptr || a.offsets == nullptr || a.row_index == nullptr || a.pos == nullptr ||
+        a.wq_gu == nullptr || a.wsf_gu == nullptr || a.wq_dn == nullptr || a.wsf_dn == nullptr || a.out == nullptr)
+        return MACAQ_ERR_INVALID_ARG;
+    const void *all[] = {a.x, a.weights, a.offsets, a.row_index, a.pos, a.wq_gu, a.wsf_gu, a.wq_dn, a.wsf_dn, a.inv_gu,
+                         a.inv_dn, a.out, workspace};
+    for (const void *p : all)
+        if (!aligned16(p)) return MACAQ_ERR_ALIGNMENT;
+    if (workspace == nullptr || ws_bytes < moe_w4a16_ws(a.T, a.topk, a.I)) return MACAQ_ERR_WORKSPACE;
+    DeviceInfo dev;
+    macaq_status s = device_info(&dev);
+    if (s != MACAQ_OK) return s;
+    MoeArgs g = a;
+    g.h = static_cast<float *>(workspace);
+    g.R = a.T * a.topk;
+    s = set_smem(moe_gate_up_kernel, g.K * sizeof(float));
+    if (s == MACAQ_OK) s = set_smem(moe_down_kernel, g.I * sizeof(float));
+    if (s == MACAQ_OK)
+        s = launch(moe_gate_up_kernel, dim3(g.R, g.I / 64), dim3(kMoeThreads), g.K * sizeof(float), st, 1, g);
+    if (s == MACAQ_OK)
+        s = launch(moe_down_kernel, dim3(g.T, g.N / 128), dim3(kMoeThreads), g.I * sizeof(float), st, 1, g);
+    return s;
+}
+
+// ------------------------------------------------------------------------ low-rank adapters
+macaq_status lora_add(const LoraArgs &p, int32_t dtype, cudaStream_t st) {
+    constexpr int64_t kMax = int64_t(1) << 31;
+    if (p.M < 0 || p.M >= kMax || p.K <= 0 || p.K >= kMax || p.N <= 0 || p.N >= kMax || p.K % 8 || p.N % 8 || p.r < 8 ||
+        p.r > kLoraMaxRank || p.r % 8 || p.L < 1 || p.L > kRouteMaxExperts)
+        return MACAQ_ERR_SHAPE;
+    if (dtype != MACAQ_OUT_BF16 && dtype != MACAQ_OUT_F32) return MACAQ_ERR_INVALID_ARG;
+    const int64_t unit = dtype == MACAQ_OUT_F32 ? 4 : 8;
+    if (p.ldx < p.K || p.ldx % 8 || p.ldy < p.N || p.ldy % unit || p.ldo < p.N || p.ldo % unit || p.ldx >= kMax || p.ldy >= kMax ||
+        p.ldo >= kMax || (p.out == p.y && p.ldo != p.ldy))
+        return MACAQ_ERR_SHAPE;
+    if (p.M == 0) return MACAQ_OK;
+    if (p.y == nullptr || p.out == nullptr || p.x == nullptr || p.A == nullptr || p.B == nullptr || p.offsets == nullptr)
+        return MACAQ_ERR_INVALID_ARG;
+    if (!aligned16(p.y) || !aligned16(p.out) || !aligned16(p.x) || !aligned16(p.A) || !aligned16(p.B) || !aligned16(p.offsets) ||
+        !aligned16(p.row_index) || !aligned4(p.scale))
+        return MACAQ_ERR_ALIGNMENT;
+    DeviceInfo dev;
+    macaq_status s = device_info(&dev);
+    if (s != MACAQ_OK) return s;
+    LoraArgs g = p;
+    g.f32 = dtype == MACAQ_OUT_F32;
+    return launch(lora_add_kernel, dim3(static_cast<unsigned>(g.M)), dim3(kLoraThreads), 0, st, 1, g);
+}
+
 }  // namespace macaq
 
 // ============================================================================ C ABI
@@ -1209,5 +1357,77 @@ macaq_status macaq_device_status(int32_t *status_out, int32_t reset) {
 }
 
 void macaq_set_wait_limit_ns(uint64_t ns) { macaq::g_wait_limit_ns.store(ns ? ns : macaq::kDefaultWaitNs); }
+
+macaq_status macaq_moe_route(const void *logits, int32_t in_dtype, int64_t ld, int64_t T, int32_t E, int32_t topk,
+                             int32_t scoring, int32_t renormalize, float scale, float *weights, int32_t *ids,
+                             int32_t *group_offsets, int32_t *row_index, int32_t *pos, macaq_stream_t stream) {
+    return macaq::moe_route(logits, in_dtype, ld, T, E, topk, scoring, renormalize, scale, weights, ids, group_offsets,
+                            row_index, pos, static_cast<cudaStream_t>(stream));
+}
+
+macaq_status macaq_row_groups(const int32_t *ids, int64_t T, int32_t topk, int32_t E, int32_t *group_offsets,
+                              int32_t *row_index, int32_t *pos, macaq_stream_t stream) {
+    return macaq::row_groups(ids, T, topk, E, group_offsets, row_index, pos, static_cast<cudaStream_t>(stream));
+}
+
+size_t macaq_moe_w4a16_workspace_bytes(int64_t T, int32_t topk, int32_t E, int64_t K, int64_t I, int64_t N) {
+    if (!macaq::moe_w4a16_shape_ok(T, topk, E, K, I, N)) return 0;
+    return macaq::moe_w4a16_ws(T, topk, I);
+}
+
+macaq_status macaq_moe_w4a16(const void *X, int64_t T, int64_t K, const float *weights, int32_t topk,
+                             const int32_t *group_offsets, int32_t E, const int32_t *row_index, const int32_t *pos,
+                             const uint8_t *Wq_gu, const uint8_t *Wsf_gu, const float *inv_s_gu, int32_t had_block, int64_t I,
+                             const uint8_t *Wq_down, const uint8_t *Wsf_down, const float *inv_s_down,
+                             int32_t had_block_down, int64_t N, void *out, void *workspace, size_t ws_bytes,
+                             macaq_stream_t stream) {
+    if (!macaq::moe_w4a16_shape_ok(T, topk, E, K, I, N)) return MACAQ_ERR_SHAPE;
+    macaq::MoeArgs a{};
+    a.x = static_cast<const uint16_t *>(X);
+    a.weights = weights;
+    a.offsets = group_offsets;
+    a.row_index = row_index;
+    a.pos = pos;
+    a.wq_gu = Wq_gu;
+    a.wsf_gu = Wsf_gu;
+    a.wq_dn = Wq_down;
+    a.wsf_dn = Wsf_down;
+    a.inv_gu = inv_s_gu;
+    a.inv_dn = inv_s_down;
+    a.out = static_cast<uint16_t *>(out);
+    a.T = static_cast<int32_t>(T);
+    a.topk = topk;
+    a.E = E;
+    a.K = static_cast<int32_t>(K);
+    a.I = static_cast<int32_t>(I);
+    a.N = static_cast<int32_t>(N);
+    a.b_gu = had_block;
+    a.b_dn = had_block_down;
+    return macaq::moe_w4a16(a, workspace, ws_bytes, static_cast<cudaStream_t>(stream));
+}
+
+macaq_status macaq_lora_add(const void *Y, int64_t ldy, void *out, int64_t ldo, int32_t dtype, const void *X, int64_t ldx,
+                            int64_t M, int64_t K, int64_t N, const void *A, const void *B, int32_t r, int32_t L,
+                            const float *scale, const int32_t *group_offsets, const int32_t *row_index,
+                            macaq_stream_t stream) {
+    macaq::LoraArgs p{};
+    p.y = Y;
+    p.out = out;
+    p.x = static_cast<const uint16_t *>(X);
+    p.A = static_cast<const uint16_t *>(A);
+    p.B = static_cast<const uint16_t *>(B);
+    p.scale = scale;
+    p.offsets = group_offsets;
+    p.row_index = row_index;
+    p.ldy = ldy;
+    p.ldo = ldo;
+    p.ldx = ldx;
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.r = r;
+    p.L = L;
+    return macaq::lora_add(p, dtype, static_cast<cudaStream_t>(stream));
+}
 
 }  // extern "C"

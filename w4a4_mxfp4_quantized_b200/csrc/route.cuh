@@ -1,0 +1,231 @@
+// route.cuh -- the router of a mixture-of-experts layer and the row plan that the grouped calls take.
+//
+// Router: per token, l_e = fp32(logit_e) with NaN read as -inf (a masked expert) and +inf as the largest
+// finite fp32. The topk experts of largest l are chosen, ties to the lowest expert; a choice whose l is -inf is
+// dropped (id -1, weight 0). With m = max l and the sum over the chosen experts (renormalize) or, for softmax,
+// over all E:
+//     softmax:  p_e = exp(l_e - m),                          weight = scale * p_e / sum p
+//     sigmoid:  p_e = exp(min(l_e, 0) - c) / (1 + exp(-|l_e|)),  weight = scale * p_e / (sum p or 1)
+// where c = min(m, 0) when renormalizing (it cancels in the quotient and keeps far negative scores from
+// underflowing together) and 0 otherwise: exp(min(l, 0)) / (1 + exp(-|l|)) is the sigmoid without overflow.
+//
+// Row plan: a stable counting sort of the R = T * topk choices by group. group_offsets[g] is the first sorted
+// row of group g, pos[i] the sorted row of entry i (-1 for an id outside [0, E)), row_index[r] the token
+// (entry / topk) of sorted row r; entries of no group follow the last group in their order.
+#pragma once
+
+#include <stdint.h>
+
+#include "ptx.cuh"
+
+namespace macaq {
+
+constexpr int kRouteMaxExperts = 1024;
+constexpr int kRouteMaxTopk = 32;
+constexpr int kRouteWarps = 8;          // tokens in flight per CTA of the top-k kernel
+constexpr int kGroupThreads = 1024;     // the row plan: one CTA
+
+struct RouteArgs {
+    const void *logits;     // [T, E] bf16 or fp32, rows `ld` elements apart
+    int64_t ld;
+    int64_t T;
+    int32_t E, topk;
+    int32_t f32, sigmoid, renorm;
+    float scale;
+    float *weights;         // [T, topk]
+    int32_t *ids;           // [T, topk]
+};
+
+struct GroupArgs {
+    const int32_t *ids;     // [R]
+    int64_t R;
+    int32_t topk, E;
+    int32_t *offsets;       // [E + 1]
+    int32_t *row_index;     // [R]
+    int32_t *pos;           // [R]
+};
+
+__device__ __forceinline__ float route_logit(const RouteArgs &a, int64_t t, int e) {
+    const float v = a.f32 ? static_cast<const float *>(a.logits)[t * a.ld + e]
+                          : __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(a.logits)[t * a.ld + e]) << 16);
+    return v != v ? -INFINITY : fminf(v, 3.402823466e38f);
+}
+
+// Order-preserving map of an fp32 value (not NaN) to uint32; 0 is below every value's key.
+__device__ __forceinline__ uint32_t order_key(float v) {
+    const uint32_t u = __float_as_uint(v + 0.0f);   // -0 becomes +0: the two tie
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+__device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k); }
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
+}
+
+// One warp, one token: lane l holds the experts l, l + 32, ... as keys; each round takes the largest key by
+// a warp-wide maximum and then the lowest expert that holds it. kVpl: experts per lane.
+template <int kVpl>
+__device__ __forceinline__ void route_token(const RouteArgs &a, int64_t t, int lane) {
+    uint32_t key[kVpl];
+#pragma unroll
+    for (int v = 0; v < kVpl; ++v) {
+        const int e = v * 32 + lane;
+        key[v] = e < a.E ? order_key(route_logit(a, t, e)) : 0u;
+    }
+    const uint32_t kMasked = order_key(-INFINITY);
+    uint32_t best = 0;
+#pragma unroll
+    for (int v = 0; v < kVpl; ++v) best = max(best, key[v]);
+    best = __reduce_max_sync(0xffffffffu, best);
+    const float m = best > kMasked ? key_value(best) : 0.0f;
+    float total = 0.0f;   // softmax over all experts
+    if (!a.sigmoid && !a.renorm) {
+#pragma unroll
+        for (int v = 0; v < kVpl; ++v)
+            if (key[v] > kMasked) total += expf(key_value(key[v]) - m);
+        total = warp_sum(total);
+    }
+    int my_id = -1;
+    uint32_t my_key = kMasked;
+    for (int j = 0; j < a.topk; ++j) {
+        uint32_t k = 0;
+#pragma unroll
+        for (int v = 0; v < kVpl; ++v) k = max(k, key[v]);
+        const uint32_t top = __reduce_max_sync(0xffffffffu, k);
+        uint32_t id = 0xffffffffu;
+#pragma unroll
+        for (int v = kVpl - 1; v >= 0; --v)
+            if (key[v] == top) id = static_cast<uint32_t>(v * 32 + lane);
+        id = __reduce_min_sync(0xffffffffu, id);
+#pragma unroll
+        for (int v = 0; v < kVpl; ++v)
+            if (id == static_cast<uint32_t>(v * 32 + lane)) key[v] = 0u;   // below -inf: not taken again
+        if (lane == j && top > kMasked) {
+            my_id = static_cast<int>(id);
+            my_key = top;
+        }
+    }
+    float p = 0.0f;
+    if (my_id >= 0) {
+        const float l = key_value(my_key);
+        p = a.sigmoid ? expf(fminf(l, 0.0f) - (a.renorm ? fminf(m, 0.0f) : 0.0f)) / (1.0f + expf(-fabsf(l))) : expf(l - m);
+    }
+    if (a.renorm) total = warp_sum(p);
+    if (lane < a.topk) {
+        a.weights[t * a.topk + lane] = my_id < 0 ? 0.0f : a.scale * ((a.renorm || !a.sigmoid) ? p / total : p);
+        a.ids[t * a.topk + lane] = my_id;
+    }
+}
+
+template <int kVpl>
+__global__ void __launch_bounds__(kRouteWarps * 32) route_topk_kernel(RouteArgs a) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kRouteWarps;
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5); t < a.T; t += stride)
+        route_token<kVpl>(a, t, lane);
+}
+
+// The row plan by one CTA. Warp w owns a contiguous piece of the entries; it walks it 32 at a time, and the lanes
+// with the same group find one another (match_any), so ranks follow the entries' order and nothing is
+// atomic. Shared memory: counts [warps][E + 1] (bucket E: no group), then the buckets' first rows [E + 1].
+__global__ void __launch_bounds__(kGroupThreads) row_groups_kernel(GroupArgs a) {
+    extern __shared__ int32_t s_counts[];
+    __shared__ int32_t s_warp[32];
+    griddep_wait();
+    griddep_launch_dependents();
+    constexpr int kWarps = kGroupThreads / 32;
+    const int B = a.E + 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int32_t *mine = s_counts + warp * B;
+    for (int i = threadIdx.x; i < kWarps * B; i += kGroupThreads) s_counts[i] = 0;
+    __syncthreads();
+    const int64_t piece = ((a.R + kWarps - 1) / kWarps + 31) / 32 * 32;
+    const int64_t begin = warp * piece, end = min(a.R, begin + piece);
+    auto bucket = [&](int64_t i) {
+        const int32_t id = a.ids[i];
+        return (id >= 0 && id < a.E) ? id : a.E;
+    };
+    for (int64_t i0 = begin; i0 < end; i0 += 32) {
+        const int64_t i = i0 + lane;
+        const bool on = i < end;
+        const uint32_t live = __ballot_sync(0xffffffffu, on);
+        if (on) {
+            const int b = bucket(i);
+            const uint32_t peers = __match_any_sync(live, b);
+            if (lane == __ffs(peers) - 1) mine[b] += __popc(peers);
+        }
+        __syncwarp();
+    }
+    __syncthreads();
+    // per bucket: exclusive prefix over the warps; then an exclusive scan of the buckets' totals (one per thread,
+    // E + 1 <= 1025 buckets: the last one starts where the groups end)
+    int32_t total = 0;
+    const int b = threadIdx.x;
+    if (b < a.E)
+        for (int w = 0; w < kWarps; ++w) {
+            const int32_t c = s_counts[w * B + b];
+            s_counts[w * B + b] = total;
+            total += c;
+        }
+    if (threadIdx.x == 0) {
+        int32_t rest = 0;
+        for (int w = 0; w < kWarps; ++w) {
+            const int32_t c = s_counts[w * B + a.E];
+            s_counts[w * B + a.E] = rest;
+            rest += c;
+        }
+    }
+    int32_t x = total;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int32_t y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+    }
+    if (lane == 31) s_warp[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int32_t y = s_warp[lane];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int32_t z = __shfl_up_sync(0xffffffffu, y, d);
+            if (lane >= d) y += z;
+        }
+        s_warp[lane] = y;
+    }
+    __syncthreads();
+    int32_t *first = s_counts + kWarps * B;
+    const int32_t base = x - total + (warp > 0 ? s_warp[warp - 1] : 0);
+    if (b < a.E) {
+        first[b] = base;
+        a.offsets[b] = base;
+    }
+    if (threadIdx.x == 0) {
+        first[a.E] = s_warp[31];
+        a.offsets[a.E] = s_warp[31];
+    }
+    __syncthreads();
+    for (int64_t i0 = begin; i0 < end; i0 += 32) {
+        const int64_t i = i0 + lane;
+        const bool on = i < end;
+        const uint32_t live = __ballot_sync(0xffffffffu, on);
+        int bk = 0;
+        uint32_t peers = 0;
+        if (on) {
+            bk = bucket(i);
+            peers = __match_any_sync(live, bk);
+            const int32_t r = first[bk] + mine[bk] + __popc(peers & ((1u << lane) - 1));
+            a.pos[i] = bk < a.E ? r : -1;
+            a.row_index[r] = static_cast<int32_t>(i / a.topk);
+        }
+        __syncwarp();
+        if (on && lane == __ffs(peers) - 1) mine[bk] += __popc(peers);
+        __syncwarp();
+    }
+}
+
+}  // namespace macaq
