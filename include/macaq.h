@@ -279,6 +279,8 @@ macaq_status macaq_row_groups(const int32_t *ids, int64_t T, int32_t topk, int32
  *     x' = X[t] diag(inv_s_gu[e]) H_b;   G, U = x' dq(W'_gu[e])^T  (64-row interleaved, as macaq_linear_swiglu)
  *     h' = (silu(G) U) diag(inv_s_down[e]) H_b';   y_r = h' dq(W'_down[e])^T
  *     out[t] = bf16( sum over j of weights[t, j] * y_{pos[t, j]} ),  fp32 accumulation
+ * x' and h' enter the products in fp16, each 32 channels of a row scaled by a power of two: rounded to 11
+ * bits, or to 2^-15 of the largest magnitude in the 32 channels where that is coarser.
  *   X              device bf16 [T, K], 0 <= T <= 64 (T == 0: no-op; larger: MACAQ_ERR_SHAPE)
  *   weights, group_offsets, row_index, pos: from macaq_moe_route (or any plan with
  *                  row_index[pos[t, j]] == t and each sorted row named by at most one pos; pos outside

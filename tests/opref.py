@@ -80,8 +80,8 @@ def spread(e, b):
 
 def moe_layer(X, weights, off, row_index, pos, layer):
     """X fp64 [T, K]; layer: dict of numpy arrays wq_gu, sf_gu (row-major scales), wq_dn, sf_dn, inv_gu, inv_dn, b, b_dn.
-    Returns (out, bound): the bf16 rounding of the output, plus what rounding x' and h' to fp16 (blocks of 128 scaled to
-    their largest value) and fp32 sums of K and I terms leave, carried through the layer to first order."""
+    Returns (out, bound): the bf16 rounding of the output, plus what rounding x' and h' to fp16 (groups of 32 scaled by a
+    power of two) and fp32 sums of K and I terms leave, carried through the layer to first order."""
     T, K = X.shape
     E, I2 = layer["wq_gu"].shape[:2]
     I, N = I2 // 2, layer["wq_dn"].shape[1]
@@ -90,8 +90,9 @@ def moe_layer(X, weights, off, row_index, pos, layer):
     n = np.arange(I)
     gate, up = 128 * (n // 64) + n % 64, 128 * (n // 64) + 64 + n % 64
 
-    def fp16_blocks(v):
-        return F16 * np.abs(v) + 2.0 ** -38 * np.repeat(np.abs(v).reshape(len(v), -1, 128).max(2), 128, axis=1)
+    def fp16_groups(v):
+        # half a step of fp16: 2^-11 of the value, or 2^-25 after scaling a group's largest value to 2^-10 or more
+        return F16 * np.abs(v) + 2.0 ** -15 * np.repeat(np.abs(v).reshape(len(v), -1, 32).max(2), 32, axis=1)
 
     for e in range(E):
         rows = [r for r in range(off[e], off[e + 1]) if r in where]
@@ -100,7 +101,7 @@ def moe_layer(X, weights, off, row_index, pos, layer):
         x = X[row_index[rows]] * (layer["inv_gu"][e] if layer["inv_gu"] is not None else 1.0)
         ex = spread(9 * F32 * np.abs(x), layer["b"])
         x = rotate(x, layer["b"])
-        ex = ex + fp16_blocks(x)
+        ex = ex + fp16_groups(x)
         W = dequant(layer["wq_gu"][e], layer["sf_gu"][e])
         gu = x @ W.T
         egu = ex @ np.abs(W).T + 2 * (K / 16 + 8) * F32 * (np.abs(x) @ np.abs(W).T)
@@ -112,7 +113,7 @@ def moe_layer(X, weights, off, row_index, pos, layer):
         inv = layer["inv_dn"][e] if layer["inv_dn"] is not None else 1.0
         h, eh = h * inv, spread(eh * inv + 9 * F32 * np.abs(h * inv), layer["b_dn"])
         h = rotate(h, layer["b_dn"])
-        eh = eh + fp16_blocks(h)
+        eh = eh + fp16_groups(h)
         W = dequant(layer["wq_dn"][e], layer["sf_dn"][e])
         y, ey = h @ W.T, eh @ np.abs(W).T + 2 * (I / 16 + 64) * F32 * (np.abs(h) @ np.abs(W).T)
         for i, r in enumerate(rows):

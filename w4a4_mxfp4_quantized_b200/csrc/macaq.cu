@@ -1115,14 +1115,58 @@ macaq_status moe_route(const void *logits, int32_t in_dtype, int64_t ld, int64_t
 }
 
 // ------------------------------------------------------------------------ few-token expert layer
-size_t moe_w4a16_ws(int64_t T, int32_t topk, int64_t I) {
-    return static_cast<size_t>(T) * topk * static_cast<size_t>(I) * sizeof(float);
+// Workspace: h fp16 [R, I], its group scales [R, I / 32], y fp32 [R, N], counters [N / 128, T].
+struct MoeLayout {
+    size_t hs_off, y_off, count_off, total;
+};
+
+MoeLayout moe_layout(int64_t T, int32_t topk, int64_t I, int64_t N) {
+    const size_t R = static_cast<size_t>(T) * topk;
+    auto up = [](size_t b) { return (b + 255) / 256 * 256; };
+    MoeLayout l;
+    l.hs_off = up(R * I * 2);
+    l.y_off = l.hs_off + up(R * (I / 32) * 4);
+    l.count_off = l.y_off + up(R * N * 4);
+    l.total = l.count_off + up(static_cast<size_t>(T) * (N / 128) * 4);
+    return l;
 }
 
 bool moe_w4a16_shape_ok(int64_t T, int32_t topk, int32_t E, int64_t K, int64_t I, int64_t N) {
     return T >= 0 && T <= kMoeMaxT && topk >= 1 && topk <= kRouteMaxTopk && E >= 1 && E <= kRouteMaxExperts && K > 0 &&
            K % 128 == 0 && K <= 16384 && I > 0 && I % 128 == 0 && I <= 16384 && N > 0 && N % 128 == 0 &&
            N <= (int64_t(1) << 20);
+}
+
+// CTAs that share a block's K tiles (a cluster): as few as keep a part's panel small, more while the launch would
+// leave SMs without work and every part keeps two tiles.
+unsigned moe_parts(int tiles, int64_t blocks, int sms) {
+    unsigned p = 1;
+    while (p < 8 && (tiles + p - 1) / p > kMoeMaxPartTiles / 2) p *= 2;
+    while (p < 8 && blocks * p < 2 * static_cast<int64_t>(sms) && tiles >= 4 * static_cast<int>(p)) p *= 2;
+    return p;
+}
+
+template <typename Kernel>
+macaq_status moe_launch(Kernel k, MoeArgs g, int rows, int tiles, unsigned parts, unsigned blocks, unsigned chunks,
+                        cudaStream_t st) {
+    g.part_tiles = (tiles + static_cast<int>(parts) - 1) / static_cast<int>(parts);
+    const size_t smem = moe_smem_bytes(g.part_tiles, rows);
+    macaq_status s = set_smem(k, smem);
+    if (s != MACAQ_OK) return s;
+    return launch(k, dim3(parts, blocks, chunks), dim3(kMoeThreads), smem, st, parts, g);
+}
+
+// Both kernels with chunks of 8 kNt rows: one chunk per expert with rows, one more per 8 kNt rows of the same expert.
+template <int kNt>
+macaq_status moe_run(const MoeArgs &g, int sms, cudaStream_t st) {
+    constexpr int kRows = 8 * kNt;
+    const int32_t experts = std::min(g.E, g.R);
+    const int32_t chunks = experts + g.R / kRows;
+    const unsigned p1 = moe_parts(g.K / 128, static_cast<int64_t>(experts) * (g.I / 128), sms);
+    const unsigned p2 = moe_parts(g.I / 128, static_cast<int64_t>(experts) * (g.N / 128), sms);
+    macaq_status s = moe_launch(moe_gate_up_kernel<kNt>, g, kRows, g.K / 128, p1, g.I / 128, chunks, st);
+    if (s == MACAQ_OK) s = moe_launch(moe_down_kernel<kNt>, g, kRows, g.I / 128, p2, g.N / 128, chunks, st);
+    return s;
 }
 
 macaq_status moe_w4a16(const MoeArgs &a, void *workspace, size_t ws_bytes, cudaStream_t st) {
@@ -1136,20 +1180,19 @@ macaq_status moe_w4a16(const MoeArgs &a, void *workspace, size_t ws_bytes, cudaS
                          a.inv_dn, a.out, workspace};
     for (const void *p : all)
         if (!aligned16(p)) return MACAQ_ERR_ALIGNMENT;
-    if (workspace == nullptr || ws_bytes < moe_w4a16_ws(a.T, a.topk, a.I)) return MACAQ_ERR_WORKSPACE;
+    const MoeLayout l = moe_layout(a.T, a.topk, a.I, a.N);
+    if (workspace == nullptr || ws_bytes < l.total) return MACAQ_ERR_WORKSPACE;
     DeviceInfo dev;
     macaq_status s = device_info(&dev);
     if (s != MACAQ_OK) return s;
     MoeArgs g = a;
-    g.h = static_cast<float *>(workspace);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    g.h = reinterpret_cast<uint16_t *>(ws);
+    g.hs = reinterpret_cast<float *>(ws + l.hs_off);
+    g.y = reinterpret_cast<float *>(ws + l.y_off);
+    g.counts = reinterpret_cast<int32_t *>(ws + l.count_off);
     g.R = a.T * a.topk;
-    s = set_smem(moe_gate_up_kernel, g.K * sizeof(float));
-    if (s == MACAQ_OK) s = set_smem(moe_down_kernel, g.I * sizeof(float));
-    if (s == MACAQ_OK)
-        s = launch(moe_gate_up_kernel, dim3(g.R, g.I / 64), dim3(kMoeThreads), g.K * sizeof(float), st, 1, g);
-    if (s == MACAQ_OK)
-        s = launch(moe_down_kernel, dim3(g.T, g.N / 128), dim3(kMoeThreads), g.I * sizeof(float), st, 1, g);
-    return s;
+    return g.R <= 4 * static_cast<int64_t>(g.E) ? moe_run<1>(g, dev.sms, st) : moe_run<2>(g, dev.sms, st);
 }
 
 // ------------------------------------------------------------------------ low-rank adapters
@@ -1372,7 +1415,7 @@ macaq_status macaq_row_groups(const int32_t *ids, int64_t T, int32_t topk, int32
 
 size_t macaq_moe_w4a16_workspace_bytes(int64_t T, int32_t topk, int32_t E, int64_t K, int64_t I, int64_t N) {
     if (!macaq::moe_w4a16_shape_ok(T, topk, E, K, I, N)) return 0;
-    return macaq::moe_w4a16_ws(T, topk, I);
+    return macaq::moe_layout(T, topk, I, N).total;
 }
 
 macaq_status macaq_moe_w4a16(const void *X, int64_t T, int64_t K, const float *weights, int32_t topk,
