@@ -15,6 +15,7 @@ huawei-csl targets GGUF, vLLM and Diffusers models", glonce.com, paragraph 5):
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -323,26 +324,32 @@ def linear_w4a16(X: torch.Tensor, inv_s: torch.Tensor | None, Wq: torch.Tensor, 
     return Y
 
 
-def _arg(name: str, t: torch.Tensor, dtype, shape, dev) -> int:
-    """The pointer of a contiguous CUDA tensor on `dev` of the given type and shape (ValueError otherwise)."""
-    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
+def _bad(name: str, t: torch.Tensor, dtype, shape, dev: int):
+    raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}, got {t.dtype} "
+                     f"{tuple(t.shape)} on {t.device}")
+
+
+def _arg(name: str, t: torch.Tensor, dtype, shape, dev: int) -> int:
+    """The pointer of a contiguous tensor on CUDA device `dev` of the given type and shape (ValueError otherwise)."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _bad(name, t, dtype, shape, dev)
     return t.data_ptr()
 
 
-def _cuda(name: str, t: torch.Tensor) -> torch.device:
+def _cuda(name: str, t: torch.Tensor) -> int:
     if not t.is_cuda:
         raise ValueError(f"{name}: libmacaq takes CUDA tensors")
-    return t.device
+    return t.get_device()
 
 
-def _call(fn: str, dev: torch.device, *args) -> None:
+def _call(fn: str, dev: int, *args) -> None:
     """Calls a library function on the tensors' device (made current for the call) and its current stream."""
-    if dev.index != torch.cuda.current_device():
+    if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return _call(fn, dev, *args)
-    _check(fn, getattr(lib(), fn)(*args, _stream(dev)))
+    status = getattr(_lib or lib(), fn)(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if status:
+        raise MacaqError(fn, status)
 
 
 _ROWS_DTYPE = {torch.bfloat16: OUT_BF16, torch.float32: OUT_F32}
@@ -391,6 +398,7 @@ def row_groups(ids: torch.Tensor, E: int, *, group_offsets=None, row_index=None,
     return plan
 
 
+@functools.lru_cache(maxsize=1024)
 def moe_w4a16_workspace_bytes(T: int, topk: int, E: int, K: int, I: int, N: int) -> int:
     return int(lib().macaq_moe_w4a16_workspace_bytes(T, topk, E, K, I, N))
 
@@ -428,9 +436,9 @@ def moe_w4a16(X: torch.Tensor, weights: torch.Tensor, group_offsets: torch.Tenso
 
 def _rows(name: str, t: torch.Tensor, dtype, M: int, N: int, dev):
     """Pointer and row stride of a [M, N] tensor whose rows are contiguous."""
-    if t.dtype is not dtype or t.shape != (M, N) or t.device != dev or (N > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name}: expected a {dtype} tensor of shape {(M, N)} with contiguous rows on {dev}, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
+    if t.dtype is not dtype or t.shape != (M, N) or t.get_device() != dev or (N > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: expected a {dtype} tensor of shape {(M, N)} with contiguous rows on cuda:{dev}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr(), (t.stride(0) if M > 1 else N)
 
 

@@ -1115,19 +1115,16 @@ macaq_status moe_route(const void *logits, int32_t in_dtype, int64_t ld, int64_t
 }
 
 // ------------------------------------------------------------------------ few-token expert layer
-// Workspace: h fp16 [R, I], its group scales [R, I / 32], y fp32 [R, N], counters [N / 128, T].
+// Workspace: h fp32 [R, I], y fp32 [R, N].
 struct MoeLayout {
-    size_t hs_off, y_off, count_off, total;
+    size_t y_off, total;
 };
 
 MoeLayout moe_layout(int64_t T, int32_t topk, int64_t I, int64_t N) {
     const size_t R = static_cast<size_t>(T) * topk;
-    auto up = [](size_t b) { return (b + 255) / 256 * 256; };
     MoeLayout l;
-    l.hs_off = up(R * I * 2);
-    l.y_off = l.hs_off + up(R * (I / 32) * 4);
-    l.count_off = l.y_off + up(R * N * 4);
-    l.total = l.count_off + up(static_cast<size_t>(T) * (N / 128) * 4);
+    l.y_off = R * I * 4;   // I and N are multiples of 128
+    l.total = l.y_off + R * N * 4;
     return l;
 }
 
@@ -1137,36 +1134,43 @@ bool moe_w4a16_shape_ok(int64_t T, int32_t topk, int32_t E, int64_t K, int64_t I
            N <= (int64_t(1) << 20);
 }
 
-// CTAs that share a block's K tiles (a cluster): as few as keep a part's panel small, more while the launch would
-// leave SMs without work and every part keeps two tiles.
-unsigned moe_parts(int tiles, int64_t blocks, int sms) {
-    unsigned p = 1;
-    while (p < 8 && (tiles + p - 1) / p > kMoeMaxPartTiles / 2) p *= 2;
-    while (p < 8 && blocks * p < 2 * static_cast<int64_t>(sms) && tiles >= 4 * static_cast<int>(p)) p *= 2;
-    return p;
-}
-
-template <typename Kernel>
-macaq_status moe_launch(Kernel k, MoeArgs g, int rows, int tiles, unsigned parts, unsigned blocks, unsigned chunks,
-                        cudaStream_t st) {
-    g.part_tiles = (tiles + static_cast<int>(parts) - 1) / static_cast<int>(parts);
-    const size_t smem = moe_smem_bytes(g.part_tiles, rows);
+// Kernel 1 or 2, with column tiles for 8 kNt rows.
+template <bool kDown, int kNt, bool kDeep>
+macaq_status moe_launch(MoeArgs g, int sms, cudaStream_t st) {
+    constexpr int kSmem = 116224 - 4 * 1024;   // half an SM's shared memory, less the static arrays and the runtime's share
+    constexpr int kTable = 1024;               // room for the chunk table: a CTA meets a few chunks
+    constexpr int kStages = kDeep ? kMoeDeepStages : kMoeWideStages;
+    const int tiles = (kDown ? g.I : g.K) / 128;
+    const int64_t per_chunk = (kDown ? g.N : 2 * g.I) / 32;
+    // panel rows: what fits; a chunk has no more rows than that
+    const int fixed = moe_table_offset(kNt, kStages, tiles, 0) + kTable;
+    g.panel_rows = std::min((kSmem - fixed) / moe_row_bytes(tiles), kMoeMaxPanels * 8 * kNt);
+    if constexpr (kDeep)
+        if (g.panel_rows < std::min(8 * kNt, 4)) return moe_launch<kDown, kNt, false>(g, sms, st);
+    if (g.panel_rows < 1) return MACAQ_ERR_SHAPE;
+    g.chunk_rows = std::min(8 * kNt, g.panel_rows);
+    const int64_t chunks = std::min(g.E, g.R) + g.R / g.chunk_rows, items = chunks * per_chunk;
+    const int64_t ctas = std::min<int64_t>(items, kDeep ? sms : 2 * sms);
+    g.max_chunks = static_cast<int32_t>((items + ctas - 1) / ctas / per_chunk + 2);
+    const size_t smem = moe_table_offset(kNt, kStages, tiles, g.panel_rows) + g.max_chunks * sizeof(MoeChunk);
+    if (smem > kSmem) return MACAQ_ERR_SHAPE;
+    auto k = moe_w4a16_kernel<kDown, kNt, kDeep>;
     macaq_status s = set_smem(k, smem);
     if (s != MACAQ_OK) return s;
-    return launch(k, dim3(parts, blocks, chunks), dim3(kMoeThreads), smem, st, parts, g);
+    return launch(k, dim3(static_cast<unsigned>(ctas)), dim3(kMoeThreads), smem, st, 1, g);
 }
 
-// Both kernels with chunks of 8 kNt rows: one chunk per expert with rows, one more per 8 kNt rows of the same expert.
+// The three launches. Few tiles per warp: one CTA per SM with deeper rings, so that kernel 2 fits beside kernel 1.
 template <int kNt>
 macaq_status moe_run(const MoeArgs &g, int sms, cudaStream_t st) {
-    constexpr int kRows = 8 * kNt;
-    const int32_t experts = std::min(g.E, g.R);
-    const int32_t chunks = experts + g.R / kRows;
-    const unsigned p1 = moe_parts(g.K / 128, static_cast<int64_t>(experts) * (g.I / 128), sms);
-    const unsigned p2 = moe_parts(g.I / 128, static_cast<int64_t>(experts) * (g.N / 128), sms);
-    macaq_status s = moe_launch(moe_gate_up_kernel<kNt>, g, kRows, g.K / 128, p1, g.I / 128, chunks, st);
-    if (s == MACAQ_OK) s = moe_launch(moe_down_kernel<kNt>, g, kRows, g.I / 128, p2, g.N / 128, chunks, st);
-    return s;
+    auto deep = [&](int64_t K, int64_t rows) {
+        return std::min(g.E, g.R) * (rows / 32) * (K / 128) < kMoeTilesForTwo * 2 * kMoeWarps * static_cast<int64_t>(sms);
+    };
+    macaq_status s = deep(g.K, 2 * g.I) ? moe_launch<false, kNt, true>(g, sms, st) : moe_launch<false, kNt, false>(g, sms, st);
+    if (s == MACAQ_OK) s = deep(g.I, g.N) ? moe_launch<true, kNt, true>(g, sms, st) : moe_launch<true, kNt, false>(g, sms, st);
+    if (s != MACAQ_OK) return s;
+    const unsigned warps = static_cast<unsigned>(g.T) * (g.N / 128);
+    return launch(moe_sum_kernel, dim3((warps + kMoeSumWarps - 1) / kMoeSumWarps), dim3(32 * kMoeSumWarps), 0, st, 1, g);
 }
 
 macaq_status moe_w4a16(const MoeArgs &a, void *workspace, size_t ws_bytes, cudaStream_t st) {
@@ -1187,10 +1191,8 @@ macaq_status moe_w4a16(const MoeArgs &a, void *workspace, size_t ws_bytes, cudaS
     if (s != MACAQ_OK) return s;
     MoeArgs g = a;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    g.h = reinterpret_cast<uint16_t *>(ws);
-    g.hs = reinterpret_cast<float *>(ws + l.hs_off);
+    g.h = reinterpret_cast<float *>(ws);
     g.y = reinterpret_cast<float *>(ws + l.y_off);
-    g.counts = reinterpret_cast<int32_t *>(ws + l.count_off);
     g.R = a.T * a.topk;
     return g.R <= 4 * static_cast<int64_t>(g.E) ? moe_run<1>(g, dev.sms, st) : moe_run<2>(g, dev.sms, st);
 }

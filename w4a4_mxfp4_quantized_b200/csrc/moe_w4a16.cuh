@@ -8,12 +8,16 @@
 // Bound by HBM: every active expert's codes and scales are read once (17/32 byte a weight), and an expert has a handful of
 // rows, so the two products are streams of weights against a small operand that stays in shared memory.
 //
-// Plan. The rows of an expert are cut into chunks of up to 8 or 16 (8 when experts average four rows or fewer, so that
-// one n8 tile nearly always does). Kernel 1 takes (chunk, 128 intermediate channels), kernel 2 (chunk, 128 output
-// channels); a cluster of CTAs may share one such block, each with a part of the K tiles (128 channels), and adds its
-// partial sums through distributed shared memory. A CTA keeps its rows' operand as fp16 in shared memory (the
-// panel). Each warp streams 32 weight rows (8 rows g of each of the four 32-row quarters of a scale tile, so one
-// 16-byte scale chunk serves a lane's four rows) through its own ring of cp.async stages: no barrier between warps.
+// Plan. Three launches: gate, up and SwiGLU (kernel 1); down (kernel 2); the weighted sum of each token's choices. The rows
+// of an expert are cut into chunks of up to 8 or 16 (8 when experts average four rows or fewer, so that one n8 tile
+// nearly always does). An item is (chunk, 32 weight rows): rows 8 p + g of each of the four 32-row quarters of a scale
+// tile, so one 16-byte scale chunk serves a lane's four rows, and gate and up rows of a channel meet in one lane.
+// CTAs of 8 warps take equal contiguous ranges of the items, chunk by chunk, and cut theirs into 8 equal runs of K tiles
+// (128 channels), one per warp, wherever the cuts fall: every warp streams the same number of weights, for one token as
+// for 64. The pieces of a cut item meet in shared memory once the CTA's warps are done. The chunks' operands are
+// fp16 panels in shared memory, made before the CTA streams; each warp streams through its own ring of cp.async stages,
+// without a barrier. With few items there is one CTA per SM, so that kernel 2's CTAs fit beside kernel 1's and fill their
+// rings with weights while it runs (programmatic launch); with many, two.
 //
 // Arithmetic. m16n8k16 fp16 MMAs with weights as the 16-row operand: a lane's 32-bit word of a row (8 codes of
 // one MX group) becomes four fp16 pairs with one conversion instruction each, exactly, and needs no pass through shared or
@@ -25,15 +29,10 @@
 // without looking at them; otherwise 1/s joins the weights' scale of the group. fp16's 11 bits round x' and h' 8 times
 // finer than the output's bf16.
 //
-// Kernel 2 starts (programmatic launch) while kernel 1 drains: its CTAs find their chunk and fill their rings with weights,
-// which no kernel in flight writes, before they wait for kernel 1's rows. A token's choices are
-// added in the order j = 0, 1, ... by the CTA that writes the last of their rows (a counter per token and 128 outputs,
-// zeroed by kernel 1), so results do not depend on timing.
 // Sources: glonce.com page on MACaQ, paragraph 3 (weight-only serving) and paragraph 5 (grouped matmul);
 // aipolix.com page, paragraph 2 (the transform at the input of every linear).
 #pragma once
 
-#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -47,9 +46,11 @@ namespace macaq {
 constexpr int kMoeMaxT = 64;
 constexpr int kMoeThreads = 256;
 constexpr int kMoeWarps = kMoeThreads / 32;
-constexpr int kMoeStages = 3;
+constexpr int kMoeWideStages = 3, kMoeDeepStages = 5;   // stages of a ring with two CTAs per SM, and with one
 constexpr int kMoeStageBytes = 2048 + 128;  // 32 rows x 64 code bytes, 8 scale chunks
-constexpr int kMoeMaxPartTiles = 16;        // K tiles of one CTA: a 16-row panel takes 64 KB
+constexpr int kMoeTilesForTwo = 8;          // K tiles per warp from which two CTAs per SM are used
+constexpr int kMoeMaxPanels = 8;
+constexpr int kMoeGroupUnroll = 2;         // MX groups of a tile in straight code
 
 struct MoeArgs {
     const uint16_t *x;            // bf16 [T, K]
@@ -60,23 +61,31 @@ struct MoeArgs {
     const uint8_t *wq_gu, *wsf_gu;
     const uint8_t *wq_dn, *wsf_dn;
     const float *inv_gu, *inv_dn; // [E, K], [E, I] or nullptr
-    uint16_t *h;                  // workspace: fp16 [R, I]
-    float *hs;                    // workspace: [R, I / 32], 1 / s of every group of h
+    float *h;                     // workspace: [R, I]
     float *y;                     // workspace: [R, N]
-    int32_t *counts;              // workspace: [N / 128, T]
     uint16_t *out;                // bf16 [T, N]
     int32_t T, topk, E, K, I, N, R, b_gu, b_dn;
-    int32_t part_tiles;           // the most K tiles a CTA of the launched kernel takes
+    int32_t chunk_rows;           // rows of a chunk: 8 or 16, fewer where a panel of so many does not fit
+    int32_t panel_rows;           // rows whose panels a CTA holds at a time
+    int32_t max_chunks;           // room for the chunks of a CTA's items
 };
 
-// Dynamic shared memory of a CTA whose part has up to `tiles` K tiles and whose chunk has up to `rows` rows: panel, 1 / s
-// [tile][group][row], a flag per tile (some s is not 1), rings.
+struct MoeChunk {
+    int32_t e, row0, rows;        // expert, first sorted row, rows
+};
+
+// A panel row of `tiles` K tiles: fp16 values, then 1 / s of its groups (kept apart, after all rows).
 __host__ __device__ constexpr int moe_panel_stride(int tiles) { return tiles * 256 + 64; }   // bytes; 64 mod 128: no bank conflicts
-__host__ __device__ constexpr int moe_ring_offset(int tiles, int rows) {
-    return rows * moe_panel_stride(tiles) + tiles * 4 * rows * 4 + kMoeMaxPartTiles * 4;
+__host__ __device__ constexpr int moe_row_bytes(int tiles) { return moe_panel_stride(tiles) + tiles * 16; }
+// Dynamic shared memory: rings, first pieces of cut items (one per warp), panel rows, their 1 / s, flags [panel][tile] (some s
+// of the tile is not 1), chunk table.
+__host__ __device__ constexpr int moe_heads_offset(int stages) { return kMoeWarps * stages * kMoeStageBytes; }
+__host__ __device__ constexpr int moe_panels_offset(int nt, int stages) { return moe_heads_offset(stages) + kMoeWarps * 1024 * nt; }
+__host__ __device__ constexpr int moe_flags_offset(int nt, int stages, int tiles, int rows) {
+    return moe_panels_offset(nt, stages) + rows * moe_row_bytes(tiles);
 }
-__host__ __device__ constexpr int moe_smem_bytes(int tiles, int rows) {
-    return moe_ring_offset(tiles, rows) + kMoeWarps * kMoeStages * kMoeStageBytes;
+__host__ __device__ constexpr int moe_table_offset(int nt, int stages, int tiles, int rows) {
+    return moe_flags_offset(nt, stages, tiles, rows) + kMoeMaxPanels * tiles * 4;
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
@@ -108,7 +117,7 @@ __device__ __forceinline__ void e2m1x8_to_half(uint32_t w, uint32_t (&h)[4]) {
 // d += A (16 x 16 fp16, rows g and g + 8 per lane) x B (16 x 8 fp16)
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                  "{%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -117,90 +126,75 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
 // d = A x B
 __device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                              uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                  "{%10, %10, %10, %10};"
                  : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
-// 2^(E - 127) of the four scale bytes of a word.
-__device__ __forceinline__ void moe_scales(uint32_t word, float (&s)[4]) {
-    uint32_t lo, hi;
+// 2^(E - 127) for the scale byte c of two words.
+__device__ __forceinline__ void moe_scales(uint32_t w0, uint32_t w1, int c, float &s0, float &s1) {
+    const uint32_t two = __byte_perm(w0, w1, 0x0040u + 0x0011u * c);
+    uint32_t r;
     asm("{\n\t.reg .b16 a, b;\n\t"
-        "mov.b32 {a, b}, %2;\n\t"
-        "cvt.rn.bf16x2.ue8m0x2 %0, a;\n\t"
-        "cvt.rn.bf16x2.ue8m0x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(word));
-    s[0] = __uint_as_float(lo << 16);
-    s[1] = __uint_as_float(lo & 0xFFFF0000u);
-    s[2] = __uint_as_float(hi << 16);
-    s[3] = __uint_as_float(hi & 0xFFFF0000u);
+        "mov.b32 {a, b}, %1;\n\t"
+        "cvt.rn.bf16x2.ue8m0x2 %0, a;\n\t}"
+        : "=r"(r)
+        : "r"(two));
+    s0 = __uint_as_float(r << 16);
+    s1 = __uint_as_float(r & 0xFFFF0000u);
 }
 
-struct MoeChunk {
-    int32_t e, row0, rows;   // expert, first sorted row, rows; e < 0: there is no such chunk
-};
-
-// The z-th chunk of the plan: per expert ceil(rows / kRows), in expert order. Offsets are clamped into [0, R], so rows of a
-// malformed plan stay inside the workspace. Called by the whole CTA; the plan is read past L1.
-template <int kRows>
-__device__ __forceinline__ MoeChunk moe_find_chunk(const MoeArgs &a, int z) {
+// The plan's chunks, per expert ceil(rows / chunk_rows) of them in expert order, make `blocks` items each. Returns the item range
+// of CTA c of `ctas` and fills table[] with the chunks that it meets. Offsets are clamped into [0, R], so
+// rows of a malformed plan stay inside the workspace; they are read past L1. Called by the whole CTA.
+__device__ __forceinline__ void moe_find_items(const MoeArgs &a, int c, int ctas, int blocks, MoeChunk *table, int &begin,
+                                               int &end) {
     __shared__ int32_t s_sum[kMoeWarps];
-    __shared__ MoeChunk s_chunk;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    constexpr int kPer = kRouteMaxExperts / kMoeThreads;
-    const int per = (a.E + kMoeThreads - 1) / kMoeThreads;   // experts per thread, in order
-    int32_t first[kPer], rows[kPer], mine = 0;
+    const int per = a.chunk_rows;
+    int32_t total = 0;
+    const int passes = a.E <= kMoeThreads ? 1 : 2;   // up to 512 experts one pass knows the total; else count first
+    for (int pass = 0; pass < passes; ++pass) {
+        int32_t before = 0;
+        for (int base = 0; base < a.E; base += kMoeThreads) {
+            const int e = base + threadIdx.x;
+            int32_t lo = 0, rows = 0;
+            if (e < a.E) {
+                lo = min(max(__ldcg(a.offsets + e), 0), a.R);
+                rows = max(min(max(__ldcg(a.offsets + e + 1), 0), a.R) - lo, 0);
+            }
+            const int32_t n = (rows + per - 1) / per;
+            int32_t x = n;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int e = threadIdx.x * per + i;
-        rows[i] = 0;
-        if (i < per && e < a.E) {
-            const int32_t lo = min(max(__ldcg(a.offsets + e), 0), a.R), hi = min(max(__ldcg(a.offsets + e + 1), 0), a.R);
-            first[i] = lo;
-            rows[i] = max(hi - lo, 0);
+            for (int d = 1; d < 32; d <<= 1) {
+                const int32_t y = __shfl_up_sync(0xffffffffu, x, d);
+                if (lane >= d) x += y;
+            }
+            __syncthreads();
+            if (lane == 31) s_sum[warp] = x;
+            __syncthreads();
+            int32_t at = before + x - n;
+#pragma unroll
+            for (int w = 0; w < kMoeWarps; ++w) {
+                const int32_t v = s_sum[w];
+                at += w < warp ? v : 0;
+                before += v;
+            }
+            if (pass == 0) total = before;
+            if (pass == passes - 1) {
+                const int64_t items = static_cast<int64_t>(total) * blocks;
+                begin = static_cast<int>(items * c / ctas);
+                end = static_cast<int>(items * (c + 1) / ctas);
+                const int z0 = begin / blocks;
+                end = min(end, (z0 + a.max_chunks) * blocks);   // more only where a plan lists a row twice
+                const int z1 = begin < end ? (end - 1) / blocks : -1;
+                for (int z = max(z0, at); z < at + n && z <= z1; ++z)
+                    table[z - z0] = {e, lo + (z - at) * per, min(rows - (z - at) * per, per)};
+            }
         }
-        mine += (rows[i] + kRows - 1) / kRows;
     }
-    int32_t x = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int32_t y = __shfl_up_sync(0xffffffffu, x, d);
-        if (lane >= d) x += y;
-    }
-    if (lane == 31) s_sum[warp] = x;
-    if (threadIdx.x == 0) s_chunk.e = -1;
     __syncthreads();
-    int32_t at = x - mine;
-    for (int w = 0; w < warp; ++w) at += s_sum[w];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int32_t n = (rows[i] + kRows - 1) / kRows;
-        if (z >= at && z < at + n) {
-            const int32_t skip = (z - at) * kRows;
-            s_chunk = {static_cast<int32_t>(threadIdx.x * per + i), first[i] + skip, min(rows[i] - skip, kRows)};
-        }
-        at += n;
-    }
-    __syncthreads();
-    return s_chunk;
-}
-
-// Four neighbouring channels per lane, 128 per warp: the block Hadamard of order b (stages h = 1, 2, ... in order).
-__device__ __forceinline__ void moe_rotate(float (&v)[4], int b, int lane) {
-    if (b == 1) return;
-    float a0 = v[0] + v[1], a1 = v[0] - v[1], a2 = v[2] + v[3], a3 = v[2] - v[3];
-    v[0] = a0 + a2, v[1] = a1 + a3, v[2] = a0 - a2, v[3] = a1 - a3;
-#pragma unroll
-    for (int h = 4; h < 128; h <<= 1) {
-        if (h >= b) break;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float o = __shfl_xor_sync(0xffffffffu, v[i], h / 4);
-            v[i] = (lane & (h / 4)) ? o - v[i] : v[i] + o;
-        }
-    }
 }
 
 // log2 of the power of two s that a group is scaled by before fp16, from its largest magnitude: 0 when that is in
@@ -218,14 +212,51 @@ __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// One 32-channel group per thread: x (bf16), multipliers, the block Hadamard of order kB, fp16 into the panel.
-// For kB > 32 the neighbouring lanes hold the neighbouring groups; the whole warp calls it. Returns 1 / s.
+// One K tile: acc += the stage's 32 rows x the panel's columns. kScaled: some group of the tile has s != 1; x0, x1: 1 / s of
+// this lane's two columns per column tile.
+template <int kNt, bool kScaled>
+__device__ __forceinline__ void moe_tile_mma(uint32_t codes, const uint32_t (&word)[4], const uint8_t *const (&bcol)[kNt],
+                                             const float *const (&x0)[kNt], const float *const (&x1)[kNt], int tile,
+                                             float (&acc)[2][kNt][4]) {
+#pragma unroll kMoeGroupUnroll
+    for (int c = 0; c < 4; ++c) {
+        uint32_t code[4], a[4][4];
+        ldmatrix_x4(code, codes ^ (c << 4));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) e2m1x8_to_half(code[q], a[q]);
+        float s[4];
+        moe_scales(word[0], word[1], c, s[0], s[1]);
+        moe_scales(word[2], word[3], c, s[2], s[3]);
+#pragma unroll
+        for (int n = 0; n < kNt; ++n) {
+            const uint4 b = *reinterpret_cast<const uint4 *>(bcol[n] + tile * 256 + c * 64);
+            float xa = 1.0f, xb = 1.0f;
+            if constexpr (kScaled) xa = x0[n][tile * 4 + c], xb = x1[n][tile * 4 + c];
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                float d[4];
+                mma_f16_zero(d, a[2 * m][0], a[2 * m + 1][0], a[2 * m][1], a[2 * m + 1][1], b.x, b.y);
+                mma_f16(d, a[2 * m][2], a[2 * m + 1][2], a[2 * m][3], a[2 * m + 1][3], b.z, b.w);
+                if constexpr (kScaled) {
+                    acc[m][n][0] = fmaf(d[0], s[2 * m] * xa, acc[m][n][0]);
+                    acc[m][n][1] = fmaf(d[1], s[2 * m] * xb, acc[m][n][1]);
+                    acc[m][n][2] = fmaf(d[2], s[2 * m + 1] * xa, acc[m][n][2]);
+                    acc[m][n][3] = fmaf(d[3], s[2 * m + 1] * xb, acc[m][n][3]);
+                } else {
+                    acc[m][n][0] = fmaf(d[0], s[2 * m], acc[m][n][0]);
+                    acc[m][n][1] = fmaf(d[1], s[2 * m], acc[m][n][1]);
+                    acc[m][n][2] = fmaf(d[2], s[2 * m + 1], acc[m][n][2]);
+                    acc[m][n][3] = fmaf(d[3], s[2 * m + 1], acc[m][n][3]);
+                }
+            }
+        }
+    }
+}
+
+// One 32-channel group per thread, 16 packed pairs: multipliers, the block Hadamard of order kB, fp16 into the panel. For
+// kB > 32 the neighbouring lanes hold the neighbouring groups; the whole warp calls it. Returns 1 / s.
 template <int kB>
-__device__ __forceinline__ float moe_group_to_half(const uint16_t *x, const float *mul, bool on, uint8_t *dst) {
-    uint4 raw[4];
-    load_group_global(x, raw);
-    uint64_t p[16];
-    unpack_bf16x32(raw, p);
+__device__ __forceinline__ float moe_group_to_half(uint64_t (&p)[16], const float *mul, bool on, uint8_t *dst) {
     if (mul != nullptr) {
         uint64_t mv[16];
         load_mul(mul, mv);
@@ -259,227 +290,315 @@ __device__ __forceinline__ float moe_group_to_half(const uint16_t *x, const floa
     return moe_pow2(-shift);
 }
 
-// The weight stream of one warp: 32 rows of a 128-row tile (rows 8 p + g + 32 q) over K tiles.
-struct MoeStream {
-    const uint8_t *codes;   // this lane's first 16 bytes: row 8 p + lane / 4, chunk lane % 4, of the first tile
-    const uint8_t *sf;      // this lane's scale chunk (lanes 0 .. 7) of the first tile
-    int64_t q_stride;       // 32 rows of codes
-    uint32_t ring;          // shared address of the warp's ring
-    uint32_t st;            // this lane's offset inside a stage for its stores
-    int lane;
-
-    __device__ __forceinline__ MoeStream(const uint8_t *wq, const uint8_t *wsf, int64_t row_tile, int K, int first_tile, int p,
-                                         uint32_t ring_, int lane_) {
-        lane = lane_;
-        const int g = lane >> 2, c = lane & 3;
-        codes = wq + (row_tile * 128 + 8 * p + g) * (K / 2) + first_tile * 64 + 16 * c;
-        sf = wsf + (row_tile * (K / 128) + first_tile) * 512 + (8 * p + (lane & 7)) * 16;
-        q_stride = 32 * static_cast<int64_t>(K / 2);
-        ring = ring_;
-        st = g * 64 + ((c ^ ((g >> 1) & 3)) << 4);
-    }
-    __device__ __forceinline__ void issue(int tile, int tiles) const {
-        if (tile < tiles) {
-            const uint32_t dst = ring + (tile % kMoeStages) * kMoeStageBytes;
-            const uint8_t *src = codes + tile * 64;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) cp_async16(dst + 512 * q + st, src + q * q_stride);
-            if (lane < 8) cp_async16(dst + 2048 + 16 * lane, sf + static_cast<int64_t>(tile) * 512);
-        }
-        cp_async_commit();   // an empty group keeps the count of groups equal to the count of tiles
-    }
+// The panel rows of a phase from X (kernel 1) or from h (kernel 2): `total` groups, row by row. rows: per panel row the chunk
+// (its number in the phase) and the row of X or h.
+struct MoeRow {
+    int32_t panel, source;
 };
 
-// One K tile: acc += the stage's 32 rows x the panel's columns. kScaled: some group of the tile has s != 1.
-template <int kNt, bool kScaled>
-__device__ __forceinline__ void moe_tile_mma(const uint32_t (&code)[4][4], const float (&sf)[4][4], uint32_t bcol, int stride,
-                                             const float *xs, float (&acc)[2][kNt][4]) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        uint32_t a[4][4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) e2m1x8_to_half(code[q][c], a[q]);
-#pragma unroll
-        for (int n = 0; n < kNt; ++n) {
-            uint32_t b[4];
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3])
-                         : "r"(bcol + n * 8 * stride + c * 64)
-                         : "memory");
-            float2 x = make_float2(1.0f, 1.0f);
-            if constexpr (kScaled) x = *reinterpret_cast<const float2 *>(xs + c * 8 * kNt + 8 * n);
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                float d[4];
-                mma_f16_zero(d, a[2 * m][0], a[2 * m + 1][0], a[2 * m][1], a[2 * m + 1][1], b[0], b[1]);
-                mma_f16(d, a[2 * m][2], a[2 * m + 1][2], a[2 * m][3], a[2 * m + 1][3], b[2], b[3]);
-                const float s0 = sf[2 * m][c], s1 = sf[2 * m + 1][c];
-                if constexpr (kScaled) {
-                    acc[m][n][0] = fmaf(d[0], s0 * x.x, acc[m][n][0]);
-                    acc[m][n][1] = fmaf(d[1], s0 * x.y, acc[m][n][1]);
-                    acc[m][n][2] = fmaf(d[2], s1 * x.x, acc[m][n][2]);
-                    acc[m][n][3] = fmaf(d[3], s1 * x.y, acc[m][n][3]);
-                } else {
-                    acc[m][n][0] = fmaf(d[0], s0, acc[m][n][0]);
-                    acc[m][n][1] = fmaf(d[1], s0, acc[m][n][1]);
-                    acc[m][n][2] = fmaf(d[2], s1, acc[m][n][2]);
-                    acc[m][n][3] = fmaf(d[3], s1, acc[m][n][3]);
-                }
-            }
-        }
-    }
-}
-
-// acc[2 row tiles][kNt column tiles][4] += the warp's 32 rows x the panel's columns over `tiles` K tiles. panel: shared address
-// of the first of these tiles; xs: 1 / s [tile][group][8 kNt]; scaled: the tiles' flags.
-template <int kNt>
-__device__ __forceinline__ void moe_stream_mma(const MoeStream &w, int tiles, uint32_t panel, int stride, const float *xs,
-                                               const int32_t *scaled, float (&acc)[2][kNt][4]) {
-    const int lane = w.lane, g = lane >> 2, t = lane & 3;
-    const uint32_t ld = (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);   // ldmatrix: chunk lane / 8 of row lane % 8
-    const uint32_t bcol = panel + g * stride + t * 16;
-    const float *xcol = xs + 2 * t;
+template <int kB, bool kDown>
+__device__ __forceinline__ void moe_fill_panels(const MoeArgs &a, const MoeChunk *chunks, const MoeRow *rows, int count, uint8_t *panel,
+                                                float *xs, int32_t *flags) {
+    const int width = kDown ? a.I : a.K, groups = width / 32, total = count * groups, lane = threadIdx.x & 31;
+    const int stride = moe_panel_stride(width / 128);
+    const float *inv_s = kDown ? a.inv_dn : a.inv_gu;
 #pragma unroll 1
-    for (int i = 0; i < tiles; ++i) {
-        cp_async_wait<kMoeStages - 2>();
-        __syncwarp();   // every lane's copies of tile i have landed, and every lane is done with tile i - 1
-        w.issue(i + kMoeStages - 1, tiles);
-        const uint32_t stage = w.ring + (i % kMoeStages) * kMoeStageBytes;
-        uint32_t code[4][4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) ldmatrix_x4(code[q], stage + 512 * q + ld);
-        uint32_t word[4];
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(word[0]), "=r"(word[1]), "=r"(word[2]), "=r"(word[3])
-                     : "r"(stage + 2048 + 16 * g)
-                     : "memory");
-        float sf[4][4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) moe_scales(word[q], sf[q]);
-        if (scaled[i]) moe_tile_mma<kNt, true>(code, sf, bcol + i * 256, stride, xcol + i * 32 * kNt, acc);
-        else moe_tile_mma<kNt, false>(code, sf, bcol + i * 256, stride, xcol, acc);
-    }
-}
-
-// A float4 of the same shared variable in another CTA of the cluster.
-__device__ __forceinline__ float4 cluster_ld4(const float *p, uint32_t rank) {
-    uint32_t addr;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(p)), "r"(rank));
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-
-__device__ __forceinline__ void add4(float4 &a, const float4 &b) {
-    a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
-}
-
-template <int kB>
-__device__ __forceinline__ void moe_fill_panel(const MoeArgs &a, const MoeChunk &ch, const int32_t *token, int tile0, int tiles,
-                                               uint8_t *panel, int stride, float *xs, int32_t *scaled, int panel_rows) {
-    const int lane = threadIdx.x & 31, groups = tiles * 4, total = ch.rows * groups;
     for (int base = threadIdx.x & ~31; base < total; base += kMoeThreads) {
         const int u = min(base + lane, total - 1);
         const int row = u / groups, gr = u - row * groups;
-        const int64_t k = tile0 * 128 + gr * 32;
-        const float inv = moe_group_to_half<kB>(a.x + static_cast<int64_t>(token[row]) * a.K + k,
-                                                a.inv_gu == nullptr ? nullptr : a.inv_gu + static_cast<int64_t>(ch.e) * a.K + k,
-                                                base + lane < total, panel + row * stride + gr * 64);
+        const MoeRow r = rows[row];
+        const int64_t k = gr * 32;
+        uint64_t p[16];
+        if constexpr (kDown) {
+            const float4 *src = reinterpret_cast<const float4 *>(a.h + static_cast<int64_t>(r.source) * a.I + k);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float4 f = __ldcg(src + i);
+                p[2 * i] = pk2(f.x, f.y);
+                p[2 * i + 1] = pk2(f.z, f.w);
+            }
+        } else {
+            uint4 raw[4];
+            load_group_global(a.x + static_cast<int64_t>(r.source) * a.K + k, raw);
+            unpack_bf16x32(raw, p);
+        }
+        const float *mul = inv_s == nullptr ? nullptr : inv_s + static_cast<int64_t>(chunks[r.panel].e) * width + k;
+        const float inv = moe_group_to_half<kB>(p, mul, base + lane < total, panel + row * stride + gr * 64);
         if (base + lane < total) {
-            xs[gr * panel_rows + row] = inv;
-            if (inv != 1.0f) scaled[gr >> 2] = 1;
+            xs[u] = inv;
+            if (inv != 1.0f) flags[r.panel * (width / 128) + (gr >> 2)] = 1;
         }
     }
 }
 
-// Kernel 1. Grid (parts of K = cluster, I / 128, chunks).
-template <int kNt>
-__global__ void __launch_bounds__(kMoeThreads, kNt == 1 ? 3 : 2) moe_gate_up_kernel(MoeArgs a) {
-    extern __shared__ __align__(16) uint8_t s_raw[];
-    constexpr int kRows = 8 * kNt;
-    __shared__ int32_t s_token[kRows];
-    griddep_wait();   // the plan, X and the workspace may belong to the previous kernel in the stream
-    griddep_launch_dependents();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int parts = gridDim.x, part = blockIdx.x;
-    if (part == 0 && blockIdx.y == 0 && blockIdx.z == 0)
-        for (int i = threadIdx.x; i < a.T * (a.N / 128); i += kMoeThreads) a.counts[i] = 0;
-    const int stride = moe_panel_stride(a.part_tiles);
-    float *xs = reinterpret_cast<float *>(s_raw + kRows * stride);
-    int32_t *scaled = reinterpret_cast<int32_t *>(xs + a.part_tiles * 4 * kRows);
-    uint8_t *rings = s_raw + moe_ring_offset(a.part_tiles, kRows);
-    if (threadIdx.x < kMoeMaxPartTiles) scaled[threadIdx.x] = 0;
-    const MoeChunk ch = moe_find_chunk<kRows>(a, blockIdx.z);
-    if (ch.e < 0) return;   // the same for the whole cluster
-    const int kt = a.K / 128;
-    const int tile0 = part * kt / parts, tiles = (part + 1) * kt / parts - tile0;
-    const int64_t row_tiles = 2 * a.I / 128;
-    const MoeStream w(a.wq_gu, a.wsf_gu, ch.e * row_tiles + 2 * blockIdx.y + (warp >> 2), a.K, tile0, warp & 3,
-                      smem_u32(rings) + warp * kMoeStages * kMoeStageBytes, lane);
-#pragma unroll
-    for (int i = 0; i < kMoeStages - 1; ++i) w.issue(i, tiles);
-    if (threadIdx.x < kRows)
-        s_token[threadIdx.x] =
-            threadIdx.x < ch.rows ? min(max(__ldcg(a.row_index + ch.row0 + threadIdx.x), 0), a.T - 1) : 0;
-    __syncthreads();
-    switch (a.b_gu) {
-        case 1: moe_fill_panel<1>(a, ch, s_token, tile0, tiles, s_raw, stride, xs, scaled, kRows); break;
-        case 16: moe_fill_panel<16>(a, ch, s_token, tile0, tiles, s_raw, stride, xs, scaled, kRows); break;
-        case 32: moe_fill_panel<32>(a, ch, s_token, tile0, tiles, s_raw, stride, xs, scaled, kRows); break;
-        case 64: moe_fill_panel<64>(a, ch, s_token, tile0, tiles, s_raw, stride, xs, scaled, kRows); break;
-        default: moe_fill_panel<128>(a, ch, s_token, tile0, tiles, s_raw, stride, xs, scaled, kRows); break;
+// The weight stream of one warp: the K tiles of consecutive items. issue() starts the copies of the next tile.
+template <int kStages>
+struct MoeStream {
+    const uint8_t *wq, *wsf;
+    const MoeChunk *table;
+    const uint8_t *codes;   // this lane's 16 bytes: row 8 p + lane / 4, chunk lane % 4
+    const uint8_t *sf;      // this lane's scale chunk (lanes 0 .. 7)
+    uint32_t ring, st;      // shared address of the warp's ring; this lane's place in a stage
+    int K, tiles, per_chunk;
+    int z, r, tile, left, slot;
+
+    __device__ __forceinline__ void point() {   // item r of chunk z: 128-row tile r / 4, p = r % 4
+        const int lane = threadIdx.x & 31;
+        const int64_t rt = static_cast<int64_t>(table[z].e) * (per_chunk / 4) + (r >> 2);
+        codes = wq + (rt * 128 + 8 * (r & 3) + (lane >> 2)) * (K / 2) + tile * 64 + 16 * (lane & 3);
+        sf = wsf + (rt * tiles + tile) * 512 + (8 * (r & 3) + (lane & 7)) * 16;
     }
-    __syncthreads();
-    float acc[2][kNt][4] = {};
-    moe_stream_mma<kNt>(w, tiles, smem_u32(s_raw), stride, xs, scaled, acc);
-    cp_async_wait<0>();
-    __syncthreads();
-    // partial sums [column][gate, up][128 channels], over the rings. Quarters 0, 1 of a warp's rows are gate channels
-    // c, c + 32; quarters 2, 3 the up rows of the same channels.
-    float *part_sums = reinterpret_cast<float *>(rings);
-    const int channel = 64 * (warp >> 2) + 8 * (warp & 3) + (lane >> 2);
+    // `count` tiles from tile `tile_` of item r_ of chunk z_ on
+    __device__ __forceinline__ void start(int z_, int r_, int tile_, int count) {
+        z = z_, r = r_, tile = tile_, left = count, slot = 0;
+        if (left > 0) point();
+#pragma unroll 1
+        for (int i = 0; i < kStages - 1; ++i) issue();
+    }
+    __device__ __forceinline__ void issue() {
+        const int lane = threadIdx.x & 31;
+        if (left > 0) {
+            const uint32_t dst = ring + slot * kMoeStageBytes;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) cp_async16(dst + 512 * q + st, codes + q * (16 * static_cast<int64_t>(K)));
+            if (lane < 8) cp_async16(dst + 2048 + 16 * lane, sf);
+            codes += 64;
+            sf += 512;
+            --left;
+            if (++tile == tiles) {
+                tile = 0;
+                if (++r == per_chunk) {
+                    r = 0;
+                    ++z;
+                }
+                if (left > 0) point();
+            }
+        }
+        slot = slot == kStages - 1 ? 0 : slot + 1;
+        cp_async_commit();   // an empty group keeps groups and stages in step
+    }
+};
+
+// An item's sums, to h (kernel 1) or y (kernel 2). A lane holds rows g of quarters 2 m + k / 2, columns 8 n + 2 t + k % 2.
+template <bool kDown, int kNt>
+__device__ __forceinline__ void moe_store_item(const MoeArgs &a, const MoeChunk &ch, int r, const float (&acc)[2][kNt][4], int lane) {
+    const int base = (kDown ? 128 : 64) * (r >> 2) + 8 * (r & 3) + (lane >> 2);
 #pragma unroll
     for (int n = 0; n < kNt; ++n)
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int k = 0; k < 4; ++k) {
+            const int col = 8 * n + 2 * (lane & 3) + (k & 1);
+            if (col >= ch.rows) continue;
+            const int64_t row = ch.row0 + col;
+            if constexpr (kDown) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                part_sums[(8 * n + 2 * (lane & 3) + (k & 1)) * 256 + m * 128 + channel + 32 * (k >> 1)] = acc[m][n][k];
-    if (parts > 1) cluster_sync();
-    else __syncthreads();
-    // rows part, part + parts, ... : one per warp and step, four channels per lane
-    for (int row = part + parts * warp; row < ch.rows; row += parts * kMoeWarps) {
-        const float *p = part_sums + row * 256 + 4 * lane;
-        float4 g = make_float4(0.0f, 0.0f, 0.0f, 0.0f), u = g;
-        for (int r = 0; r < parts; ++r) {
-            add4(g, parts > 1 ? cluster_ld4(p, r) : *reinterpret_cast<const float4 *>(p));
-            add4(u, parts > 1 ? cluster_ld4(p + 128, r) : *reinterpret_cast<const float4 *>(p + 128));
+                for (int m = 0; m < 2; ++m) a.y[row * a.N + base + 32 * (2 * m + (k >> 1))] = acc[m][n][k];
+            } else {   // quarters 0, 1: gate rows of channels c, c + 32; quarters 2, 3: their up rows
+                const float v = acc[0][n][k];
+                a.h[row * a.I + base + 32 * (k >> 1)] = v / (1.0f + expf(-v)) * acc[1][n][k];
+            }
         }
-        float v[4] = {g.x / (1.0f + expf(-g.x)) * u.x, g.y / (1.0f + expf(-g.y)) * u.y, g.z / (1.0f + expf(-g.z)) * u.z,
-                      g.w / (1.0f + expf(-g.w)) * u.w};
-        const int i = 128 * blockIdx.y + 4 * lane;
-        if (a.inv_dn != nullptr) {
-            const float4 f = *reinterpret_cast<const float4 *>(a.inv_dn + static_cast<int64_t>(ch.e) * a.I + i);
-            v[0] *= f.x, v[1] *= f.y, v[2] *= f.z, v[3] *= f.w;
-        }
-        moe_rotate(v, a.b_dn, lane);
-        float top = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
-#pragma unroll
-        for (int d = 1; d < 8; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));   // 8 lanes: a group
-        const int shift = moe_shift(top);
-        const float s = moe_pow2(shift);
-        const int64_t r = ch.row0 + row;
-        *reinterpret_cast<uint2 *>(a.h + r * a.I + i) = make_uint2(half2_bits(v[0] * s, v[1] * s), half2_bits(v[2] * s, v[3] * s));
-        if ((lane & 7) == 0) a.hs[r * (a.I / 32) + i / 32] = moe_pow2(-shift);
-    }
-    if (parts > 1) cluster_sync();   // no CTA leaves while another reads its sums
 }
 
-// The sum of a token's choices for 128 outputs, four per lane, in the order of the choices.
-__device__ __forceinline__ void moe_combine_token(const MoeArgs &a, int t, int n, int lane) {
+// kDown = false: kernel 1; true: kernel 2. kDeep: one CTA per SM and few tiles per warp, where a launch is mostly
+// latency. A deep kernel goes through its panel and tile code once on whatever is in memory before it waits for the kernel
+// ahead of it, so that the instructions are cached when the operands arrive; what that pass computes is dropped. Measured
+// for one token of 128 experts, top-8, 2048 x 768: the first tile after the wait took 2.2 us without the pass.
+template <bool kDown, int kNt, bool kDeep>
+__global__ void __launch_bounds__(kMoeThreads, 2) moe_w4a16_kernel(MoeArgs a) {
+    constexpr int kStages = kDeep ? kMoeDeepStages : kMoeWideStages;
+    extern __shared__ __align__(128) uint8_t s_raw[];
+    __shared__ MoeRow s_rows[kMoeMaxPanels * 8 * kNt];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    if constexpr (kDown) griddep_launch_dependents();
+
+    const int kt = (kDown ? a.I : a.K) / 128, stride = moe_panel_stride(kt);
+    float *heads = reinterpret_cast<float *>(s_raw + moe_heads_offset(kStages));
+    uint8_t *panel = s_raw + moe_panels_offset(kNt, kStages);
+    float *xs = reinterpret_cast<float *>(panel + a.panel_rows * stride);   // [row][group]
+    int32_t *flags = reinterpret_cast<int32_t *>(s_raw + moe_flags_offset(kNt, kStages, kt, a.panel_rows));
+    MoeChunk *table = reinterpret_cast<MoeChunk *>(s_raw + moe_table_offset(kNt, kStages, kt, a.panel_rows));
+
+    MoeStream<kStages> w;
+    w.wq = kDown ? a.wq_dn : a.wq_gu;
+    w.wsf = kDown ? a.wsf_dn : a.wsf_gu;
+    w.table = table;
+    w.ring = smem_u32(s_raw) + warp * kStages * kMoeStageBytes;
+    w.st = g * 64 + ((t ^ ((g >> 1) & 3)) << 4);
+    w.K = 128 * kt;
+    w.tiles = kt;
+    w.per_chunk = (kDown ? a.N : 2 * a.I) / 32;
+    const uint32_t ld = (lane >> 3) * 512 + (lane & 7) * 64 + (((lane >> 1) & 3) << 4);   // ldmatrix: row lane % 8 of quarter lane / 8
+
+    int begin = 0, end = 0, from = 0, to = 0;   // items: of the CTA, of the phase
+    int z = 0, r = 0;                           // item `from` is number r of the table's chunk z
+    int chunks = 1, rows = 1, total = 0, first = 0, last = 1, tile = 0, item_z = 0, item_r = 0;
+    bool found = false, prepared = false, dry = kDeep;
+    for (;;) {
+        // Kernel 1 waits for everything before it and only then lets kernel 2 start, so the plan and the weights are
+        // complete for both; kernel 2 waits for kernel 1's rows before it reads them.
+        if (!found && (kDown || !dry)) {
+            if constexpr (!kDown) {
+                griddep_wait();
+                griddep_launch_dependents();
+            }
+            moe_find_items(a, blockIdx.x, gridDim.x, w.per_chunk, table, begin, end);
+            from = begin;
+            r = begin % w.per_chunk;
+            found = true;
+        }
+        auto cut = [&](int i) { return static_cast<int>(static_cast<int64_t>(total) * i / kMoeWarps); };
+        if (found && !prepared) {
+            if (from >= end) break;
+            // a phase: the items of as many chunks as have their panel rows in shared memory at a time
+            chunks = rows = 0;
+            to = from;
+            while (to < end && chunks < kMoeMaxPanels && rows + table[z + chunks].rows <= a.panel_rows) {
+                rows += table[z + chunks].rows;
+                to = min(end, to + w.per_chunk - (chunks == 0 ? r : 0));
+                ++chunks;
+            }
+            total = (to - from) * kt;
+            first = cut(warp), last = cut(warp + 1);
+            tile = first % kt;   // where this warp starts
+            item_r = r + first / kt;
+            item_z = z + item_r / w.per_chunk;
+            item_r %= w.per_chunk;
+            w.start(item_z, item_r, tile, last - first);
+            for (int i = threadIdx.x; i < chunks * 8 * kNt; i += kMoeThreads) {
+                int at = i % (8 * kNt);
+                const MoeChunk ch = table[z + i / (8 * kNt)];
+                if (at >= ch.rows) continue;
+                const int src = kDown ? ch.row0 + at : min(max(__ldcg(a.row_index + ch.row0 + at), 0), a.T - 1);
+                for (int c = 0; c < i / (8 * kNt); ++c) at += table[z + c].rows;
+                s_rows[at] = {i / (8 * kNt), src};
+            }
+            prepared = true;
+        }
+        if (!found && threadIdx.x == 0) {   // kernel 1's dry pass: row 0 of X
+            table[0] = {0, 0, 1};
+            s_rows[0] = {0, 0};
+        }
+        for (int i = threadIdx.x; i < chunks * kt; i += kMoeThreads) flags[i] = 0;
+        if constexpr (kDown)
+            if (!dry && from == begin) griddep_wait();
+        __syncthreads();
+        const int fill = dry ? 1 : rows;
+        switch (kDown ? a.b_dn : a.b_gu) {
+            case 1: moe_fill_panels<1, kDown>(a, table + z, s_rows, fill, panel, xs, flags); break;
+            case 16: moe_fill_panels<16, kDown>(a, table + z, s_rows, fill, panel, xs, flags); break;
+            case 32: moe_fill_panels<32, kDown>(a, table + z, s_rows, fill, panel, xs, flags); break;
+            case 64: moe_fill_panels<64, kDown>(a, table + z, s_rows, fill, panel, xs, flags); break;
+            default: moe_fill_panels<128, kDown>(a, table + z, s_rows, fill, panel, xs, flags); break;
+        }
+        __syncthreads();
+
+        float acc[2][kNt][4] = {};
+        bool whole = tile == 0;   // the piece in acc starts its item
+        const uint8_t *bcol[kNt];
+        const float *x0[kNt], *x1[kNt];
+        const int32_t *flag = nullptr;
+        auto open = [&]() {
+            int base = 0;
+            for (int c = z; c < item_z; ++c) base += table[c].rows;
+            const int most = table[item_z].rows - 1;   // columns past the chunk's rows read its last row and go nowhere
+#pragma unroll
+            for (int n = 0; n < kNt; ++n) {
+                bcol[n] = panel + (base + min(8 * n + g, most)) * stride + t * 16;
+                x0[n] = xs + (base + min(8 * n + 2 * t, most)) * kt * 4;
+                x1[n] = xs + (base + min(8 * n + 2 * t + 1, most)) * kt * 4;
+            }
+            flag = flags + (item_z - z) * kt;
+        };
+        if (first < last) open();
+        int slot = 0;
+#pragma unroll 1
+        for (int j = first; j < last; ++j) {
+            if (!dry) {
+                cp_async_wait<kStages - 2>();
+                __syncwarp();   // every lane's copies of this tile have landed, and every lane is done with the tile before
+                w.issue();
+            }
+            const uint32_t stage = w.ring + slot * kMoeStageBytes;
+            slot = slot == kStages - 1 ? 0 : slot + 1;
+            uint32_t word[4];
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(word[0]), "=r"(word[1]), "=r"(word[2]), "=r"(word[3])
+                         : "r"(stage + 2048 + 16 * g)
+                         : "memory");
+            if (flag[tile]) moe_tile_mma<kNt, true>(stage + ld, word, bcol, x0, x1, tile, acc);
+            else moe_tile_mma<kNt, false>(stage + ld, word, bcol, x0, x1, tile, acc);
+            if (dry) break;
+            if (++tile == kt) {
+                if (whole) {
+                    moe_store_item<kDown, kNt>(a, table[item_z], item_r, acc, lane);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8 * kNt; ++i) heads[(warp * 8 * kNt + i) * 32 + lane] = acc[i / (4 * kNt)][i / 4 % kNt][i % 4];
+                }
+#pragma unroll
+                for (int i = 0; i < 8 * kNt; ++i) acc[i / (4 * kNt)][i / 4 % kNt][i % 4] = 0.0f;
+                tile = 0;
+                whole = true;
+                if (++item_r == w.per_chunk) {
+                    item_r = 0;
+                    ++item_z;
+                    if (j + 1 < last) open();
+                }
+            }
+        }
+        float *tails = reinterpret_cast<float *>(s_raw + warp * kStages * kMoeStageBytes);
+        if (dry) {
+            // keeps the dry pass's sums: the condition never holds (the panel's stride is not 1)
+            if (stride == 1) heads[lane] = acc[0][0][0] + acc[1][0][1] + acc[0][0][2] + acc[1][0][3];
+            dry = false;
+            __syncthreads();
+            continue;
+        }
+        cp_async_wait<0>();
+        __syncwarp();
+        // a piece that its item's end does not close: the warp's first if it starts inside the item, else over its ring
+        if (tile != 0 && first < last) {
+            float *dst = whole ? tails : heads + warp * 8 * kNt * 32;
+#pragma unroll
+            for (int i = 0; i < 8 * kNt; ++i) dst[i * 32 + lane] = acc[i / (4 * kNt)][i / 4 % kNt][i % 4];
+        }
+        __syncthreads();
+        // a cut item is closed by the first warp that starts inside it: the piece before, its own, and those after
+        if (first % kt != 0 && warp > 0 && cut(warp - 1) <= first / kt * kt) {
+            const int stop = (first / kt + 1) * kt;
+            const float *before = reinterpret_cast<const float *>(s_raw + (warp - 1) * kStages * kMoeStageBytes);
+#pragma unroll
+            for (int i = 0; i < 8 * kNt; ++i) acc[i / (4 * kNt)][i / 4 % kNt][i % 4] = before[i * 32 + lane];
+            for (int v = warp; v < kMoeWarps && cut(v) < stop; ++v) {
+                if (cut(v) == cut(v + 1)) continue;
+#pragma unroll
+                for (int i = 0; i < 8 * kNt; ++i) acc[i / (4 * kNt)][i / 4 % kNt][i % 4] += heads[(v * 8 * kNt + i) * 32 + lane];
+            }
+            const int it = r + first / kt;
+            moe_store_item<kDown, kNt>(a, table[z + it / w.per_chunk], it % w.per_chunk, acc, lane);
+        }
+        r = (r + to - from) % w.per_chunk;
+        z += r == 0 ? chunks : chunks - 1;
+        from = to;
+        prepared = false;
+        __syncthreads();   // panels and pieces are read before the next phase writes them
+    }
+    if constexpr (kDown)
+        if (begin >= end) griddep_wait();   // nothing after this grid runs before kernel 1 ends
+}
+
+// The weighted sum of each token's choices, in the order j = 0, 1, ...: a warp takes 128 outputs of a token.
+constexpr int kMoeSumWarps = 4;
+__global__ void __launch_bounds__(32 * kMoeSumWarps) moe_sum_kernel(MoeArgs a) {
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31, blocks = a.N / 128;
+    const int id = blockIdx.x * kMoeSumWarps + (threadIdx.x >> 5);
+    if (id >= a.T * blocks) {
+        griddep_wait();
+        return;
+    }
+    const int t = id / blocks, n = 128 * (id - t * blocks) + 4 * lane;
     const int32_t live = min(max(__ldcg(a.offsets + a.E), 0), a.R);
     int32_t p = -1;
     float wt = 0.0f;
@@ -488,126 +607,27 @@ __device__ __forceinline__ void moe_combine_token(const MoeArgs &a, int t, int n
         wt = __ldcg(a.weights + t * a.topk + lane);
         if (p >= live) p = -1;
     }
-    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-    for (int j = 0; j < a.topk; ++j) {
-        const int32_t r = __shfl_sync(0xffffffffu, p, j);
-        const float w = __shfl_sync(0xffffffffu, wt, j);
-        if (r >= 0) {
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.y + static_cast<int64_t>(r) * a.N + n + 4 * lane));
-            s.x = fmaf(w, v.x, s.x), s.y = fmaf(w, v.y, s.y), s.z = fmaf(w, v.z, s.z), s.w = fmaf(w, v.w, s.w);
+    griddep_wait();   // the rows of kernel 2; the plan is older
+    float s[4] = {};
+    for (int j0 = 0; j0 < a.topk; j0 += 8) {
+        float4 u[8];
+        float wj[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {   // eight rows in flight
+            const int32_t r = __shfl_sync(0xffffffffu, p, (j0 + j) & 31);
+            wj[j] = __shfl_sync(0xffffffffu, wt, (j0 + j) & 31);
+            u[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (j0 + j < a.topk && r >= 0) u[j] = __ldcg(reinterpret_cast<const float4 *>(a.y + static_cast<int64_t>(r) * a.N + n));
+            else wj[j] = 0.0f;
         }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            s[0] = fmaf(wj[j], u[j].x, s[0]), s[1] = fmaf(wj[j], u[j].y, s[1]), s[2] = fmaf(wj[j], u[j].z, s[2]),
+            s[3] = fmaf(wj[j], u[j].w, s[3]);
     }
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x, s.y), hi = __floats2bfloat162_rn(s.z, s.w);
-    *reinterpret_cast<uint2 *>(a.out + static_cast<int64_t>(t) * a.N + n + 4 * lane) =
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(s[0], s[1]), hi = __floats2bfloat162_rn(s[2], s[3]);
+    *reinterpret_cast<uint2 *>(a.out + static_cast<int64_t>(t) * a.N + n) =
         make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
-}
-
-// Live choices of token t (whole warp): how many rows its counter waits for.
-__device__ __forceinline__ int moe_live_choices(const MoeArgs &a, int t, int32_t live, int lane) {
-    const int32_t p = lane < a.topk ? __ldcg(a.pos + t * a.topk + lane) : -1;
-    return __popc(__ballot_sync(0xffffffffu, p >= 0 && p < live));
-}
-
-// Kernel 2. Grid (parts of I = cluster, N / 128, chunks). Warps 0-3 and 4-7 take the halves of the part's tiles for the same
-// 128 rows.
-template <int kNt>
-__global__ void __launch_bounds__(kMoeThreads, kNt == 1 ? 3 : 2) moe_down_kernel(MoeArgs a) {
-    constexpr int kRows = 8 * kNt;
-    extern __shared__ __align__(16) uint8_t s_raw[];
-    __shared__ int32_t s_token[kRows];
-    __shared__ int32_t s_need[kRows];
-    __shared__ int32_t s_last[kRows];
-    griddep_launch_dependents();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int parts = gridDim.x, part = blockIdx.x;
-    // Kernel 1 let this grid start only after its own wait for everything before it, so the plan and the weights are
-    // complete; only kernel 1's rows are not.
-    const MoeChunk ch = moe_find_chunk<kRows>(a, blockIdx.z);
-    const int32_t live = min(max(__ldcg(a.offsets + a.E), 0), a.R);
-    if (part == 0 && blockIdx.z == 0)   // tokens whose choices are all dropped
-        for (int t = warp; t < a.T; t += kMoeWarps)
-            if (moe_live_choices(a, t, live, lane) == 0) {
-                griddep_wait();
-                *reinterpret_cast<uint2 *>(a.out + static_cast<int64_t>(t) * a.N + 128 * blockIdx.y + 4 * lane) = make_uint2(0u, 0u);
-            }
-    if (ch.e < 0) {
-        griddep_wait();
-        return;
-    }
-    const int kt = a.I / 128;
-    const int tile0 = part * kt / parts, tiles = (part + 1) * kt / parts - tile0;
-    const int half0 = (warp >> 2) ? tiles / 2 : 0, halves = (warp >> 2) ? tiles - tiles / 2 : tiles / 2;
-    const int stride = moe_panel_stride(a.part_tiles);
-    float *xs = reinterpret_cast<float *>(s_raw + kRows * stride);
-    int32_t *scaled = reinterpret_cast<int32_t *>(xs + a.part_tiles * 4 * kRows);
-    uint8_t *rings = s_raw + moe_ring_offset(a.part_tiles, kRows);
-    if (threadIdx.x < kMoeMaxPartTiles) scaled[threadIdx.x] = 0;
-    const MoeStream w(a.wq_dn, a.wsf_dn, ch.e * static_cast<int64_t>(a.N / 128) + blockIdx.y, a.I, tile0 + half0, warp & 3,
-                      smem_u32(rings) + warp * kMoeStages * kMoeStageBytes, lane);
-#pragma unroll
-    for (int i = 0; i < kMoeStages - 1; ++i) w.issue(i, halves);
-    for (int row = warp; row < ch.rows; row += kMoeWarps) {
-        const int t = min(max(__ldcg(a.row_index + ch.row0 + row), 0), a.T - 1);
-        const int need = moe_live_choices(a, t, live, lane);
-        if (lane == 0) {
-            s_token[row] = t;
-            s_need[row] = need;
-        }
-    }
-    griddep_wait();
-    __syncthreads();
-    for (int i = threadIdx.x; i < ch.rows * tiles * 16; i += kMoeThreads) {
-        const int row = i / (tiles * 16), c = i - row * tiles * 16;
-        *reinterpret_cast<uint4 *>(s_raw + row * stride + c * 16) =
-            __ldcg(reinterpret_cast<const uint4 *>(a.h + static_cast<int64_t>(ch.row0 + row) * a.I + tile0 * 128 + c * 8));
-    }
-    for (int i = threadIdx.x; i < ch.rows * tiles * 4; i += kMoeThreads) {
-        const int row = i / (tiles * 4), gr = i - row * tiles * 4;
-        const float inv = __ldcg(a.hs + static_cast<int64_t>(ch.row0 + row) * (a.I / 32) + tile0 * 4 + gr);
-        xs[gr * kRows + row] = inv;
-        if (inv != 1.0f) scaled[gr >> 2] = 1;
-    }
-    __syncthreads();
-    float acc[2][kNt][4] = {};
-    moe_stream_mma<kNt>(w, halves, smem_u32(s_raw) + half0 * 256, stride, xs + half0 * 4 * kRows, scaled + half0, acc);
-    cp_async_wait<0>();
-    __syncthreads();
-    float *part_sums = reinterpret_cast<float *>(rings);   // [halves][column][128]
-#pragma unroll
-    for (int n = 0; n < kNt; ++n)
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)   // quarter 2 m + k / 2, column 2 t + k % 2
-                part_sums[((warp >> 2) * kRows + 8 * n + 2 * (lane & 3) + (k & 1)) * 128 + 8 * (warp & 3) + (lane >> 2) +
-                          32 * (2 * m + (k >> 1))] = acc[m][n][k];
-    if (parts > 1) cluster_sync();
-    else __syncthreads();
-    const int n = 128 * blockIdx.y;
-    for (int row = part + parts * warp; row < ch.rows; row += parts * kMoeWarps) {
-        const float *p = part_sums + row * 128 + 4 * lane;
-        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int r = 0; r < parts; ++r) {
-            add4(s, parts > 1 ? cluster_ld4(p, r) : *reinterpret_cast<const float4 *>(p));
-            add4(s, parts > 1 ? cluster_ld4(p + kRows * 128, r) : *reinterpret_cast<const float4 *>(p + kRows * 128));
-        }
-        *reinterpret_cast<float4 *>(a.y + static_cast<int64_t>(ch.row0 + row) * a.N + n + 4 * lane) = s;
-    }
-    // whoever counts a token's last row adds its choices: rows are visible on the device before they are counted
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x < ch.rows && threadIdx.x % parts == part) {
-        const int t = s_token[threadIdx.x];
-        s_last[threadIdx.x] = atomicAdd(a.counts + static_cast<int64_t>(blockIdx.y) * a.T + t, 1) + 1 == s_need[threadIdx.x];
-    }
-    __syncthreads();
-    for (int row = part + parts * warp; row < ch.rows; row += parts * kMoeWarps)
-        if (s_last[row]) {
-            __threadfence();
-            moe_combine_token(a, s_token[row], n, lane);
-        }
-    if (parts > 1) cluster_sync();
 }
 
 }  // namespace macaq
