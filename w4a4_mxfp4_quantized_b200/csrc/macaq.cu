@@ -1137,34 +1137,34 @@ bool moe_w4a16_shape_ok(int64_t T, int32_t topk, int32_t E, int64_t K, int64_t I
 // Kernel 1 or 2, with column tiles for 8 kNt rows.
 template <bool kDown, int kNt, bool kDeep>
 macaq_status moe_launch(MoeArgs g, int sms, cudaStream_t st) {
-    constexpr int kSmem = 116224 - 4 * 1024;   // half an SM's shared memory, less the static arrays and the runtime's share
-    constexpr int kTable = 1024;               // room for the chunk table: a CTA meets a few chunks
-    constexpr int kStages = kDeep ? kMoeDeepStages : kMoeWideStages;
+    // shared memory of a CTA: an SM's, or half, less the static arrays and the runtime's share
+    constexpr int kSmem = (kDeep ? 116224 : 232448) - 4 * 1024;
+    constexpr int kTable = 1024;   // room for the chunk table: a CTA meets a few chunks
     const int tiles = (kDown ? g.I : g.K) / 128;
     const int64_t per_chunk = (kDown ? g.N : 2 * g.I) / 32;
     // panel rows: what fits; a chunk has no more rows than that
-    const int fixed = moe_table_offset(kNt, kStages, tiles, 0) + kTable;
+    const int fixed = moe_table_offset(kNt, kDeep, tiles, 0) + kTable;
     g.panel_rows = std::min((kSmem - fixed) / moe_row_bytes(tiles), kMoeMaxPanels * 8 * kNt);
     if constexpr (kDeep)
-        if (g.panel_rows < std::min(8 * kNt, 4)) return moe_launch<kDown, kNt, false>(g, sms, st);
+        if (g.panel_rows < (kNt == 1 ? 4 : 24)) return moe_launch<kDown, kNt, false>(g, sms, st);   // would take phases
     if (g.panel_rows < 1) return MACAQ_ERR_SHAPE;
     g.chunk_rows = std::min(8 * kNt, g.panel_rows);
     const int64_t chunks = std::min(g.E, g.R) + g.R / g.chunk_rows, items = chunks * per_chunk;
-    const int64_t ctas = std::min<int64_t>(items, kDeep ? sms : 2 * sms);
+    const int64_t ctas = std::min<int64_t>(items, sms);
     g.max_chunks = static_cast<int32_t>((items + ctas - 1) / ctas / per_chunk + 2);
-    const size_t smem = moe_table_offset(kNt, kStages, tiles, g.panel_rows) + g.max_chunks * sizeof(MoeChunk);
+    const size_t smem = moe_table_offset(kNt, kDeep, tiles, g.panel_rows) + g.max_chunks * sizeof(MoeChunk);
     if (smem > kSmem) return MACAQ_ERR_SHAPE;
     auto k = moe_w4a16_kernel<kDown, kNt, kDeep>;
     macaq_status s = set_smem(k, smem);
     if (s != MACAQ_OK) return s;
-    return launch(k, dim3(static_cast<unsigned>(ctas)), dim3(kMoeThreads), smem, st, 1, g);
+    return launch(k, dim3(static_cast<unsigned>(ctas)), dim3(32 * (kDeep ? kMoeDeepWarps : kMoeWideWarps)), smem, st, 1, g);
 }
 
-// The three launches. Few tiles per warp: one CTA per SM with deeper rings, so that kernel 2 fits beside kernel 1.
+// The three launches; the deep kernels where an SM has few tiles.
 template <int kNt>
 macaq_status moe_run(const MoeArgs &g, int sms, cudaStream_t st) {
     auto deep = [&](int64_t K, int64_t rows) {
-        return std::min(g.E, g.R) * (rows / 32) * (K / 128) < kMoeTilesForTwo * 2 * kMoeWarps * static_cast<int64_t>(sms);
+        return std::min(g.E, g.R) * (rows / 32) * (K / 128) < kMoeWideTiles * static_cast<int64_t>(sms);
     };
     macaq_status s = deep(g.K, 2 * g.I) ? moe_launch<false, kNt, true>(g, sms, st) : moe_launch<false, kNt, false>(g, sms, st);
     if (s == MACAQ_OK) s = deep(g.I, g.N) ? moe_launch<true, kNt, true>(g, sms, st) : moe_launch<true, kNt, false>(g, sms, st);

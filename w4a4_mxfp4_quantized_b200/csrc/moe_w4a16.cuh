@@ -12,12 +12,12 @@
 // of an expert are cut into chunks of up to 8 or 16 (8 when experts average four rows or fewer, so that one n8 tile
 // nearly always does). An item is (chunk, 32 weight rows): rows 8 p + g of each of the four 32-row quarters of a scale
 // tile, so one 16-byte scale chunk serves a lane's four rows, and gate and up rows of a channel meet in one lane.
-// CTAs of 8 warps take equal contiguous ranges of the items, chunk by chunk, and cut theirs into 8 equal runs of K tiles
+// CTAs, one per SM, take equal contiguous ranges of the items, chunk by chunk, and cut theirs into equal runs of K tiles
 // (128 channels), one per warp, wherever the cuts fall: every warp streams the same number of weights, for one token as
 // for 64. The pieces of a cut item meet in shared memory once the CTA's warps are done. The chunks' operands are
 // fp16 panels in shared memory, made before the CTA streams; each warp streams through its own ring of cp.async stages,
-// without a barrier. With few items there is one CTA per SM, so that kernel 2's CTAs fit beside kernel 1's and fill their
-// rings with weights while it runs (programmatic launch); with many, two.
+// without a barrier. "Deep" CTAs, for few items, have 8 warps and half an SM's registers and shared memory, so that
+// kernel 2's fit beside kernel 1's and fill their rings with weights while it runs (programmatic launch); others 16.
 //
 // Arithmetic. m16n8k16 fp16 MMAs with weights as the 16-row operand: a lane's 32-bit word of a row (8 codes of
 // one MX group) becomes four fp16 pairs with one conversion instruction each, exactly, and needs no pass through shared or
@@ -44,11 +44,10 @@
 namespace macaq {
 
 constexpr int kMoeMaxT = 64;
-constexpr int kMoeThreads = 256;
-constexpr int kMoeWarps = kMoeThreads / 32;
-constexpr int kMoeWideStages = 3, kMoeDeepStages = 5;   // stages of a ring with two CTAs per SM, and with one
+constexpr int kMoeDeepWarps = 8, kMoeWideWarps = 16;
+constexpr int kMoeDeepStages = 4, kMoeWideStages = 3;
 constexpr int kMoeStageBytes = 2048 + 128;  // 32 rows x 64 code bytes, 8 scale chunks
-constexpr int kMoeTilesForTwo = 8;          // K tiles per warp from which two CTAs per SM are used
+constexpr int kMoeWideTiles = 128;          // K tiles per SM from which the wide kernels are used
 constexpr int kMoeMaxPanels = 8;
 constexpr int kMoeGroupUnroll = 2;         // MX groups of a tile in straight code
 
@@ -79,13 +78,17 @@ __host__ __device__ constexpr int moe_panel_stride(int tiles) { return tiles * 2
 __host__ __device__ constexpr int moe_row_bytes(int tiles) { return moe_panel_stride(tiles) + tiles * 16; }
 // Dynamic shared memory: rings, first pieces of cut items (one per warp), panel rows, their 1 / s, flags [panel][tile] (some s
 // of the tile is not 1), chunk table.
-__host__ __device__ constexpr int moe_heads_offset(int stages) { return kMoeWarps * stages * kMoeStageBytes; }
-__host__ __device__ constexpr int moe_panels_offset(int nt, int stages) { return moe_heads_offset(stages) + kMoeWarps * 1024 * nt; }
-__host__ __device__ constexpr int moe_flags_offset(int nt, int stages, int tiles, int rows) {
-    return moe_panels_offset(nt, stages) + rows * moe_row_bytes(tiles);
+__host__ __device__ constexpr int moe_heads_offset(bool deep) {
+    return (deep ? kMoeDeepWarps * kMoeDeepStages : kMoeWideWarps * kMoeWideStages) * kMoeStageBytes;
 }
-__host__ __device__ constexpr int moe_table_offset(int nt, int stages, int tiles, int rows) {
-    return moe_flags_offset(nt, stages, tiles, rows) + kMoeMaxPanels * tiles * 4;
+__host__ __device__ constexpr int moe_panels_offset(int nt, bool deep) {
+    return moe_heads_offset(deep) + (deep ? kMoeDeepWarps : kMoeWideWarps) * 1024 * nt;
+}
+__host__ __device__ constexpr int moe_flags_offset(int nt, bool deep, int tiles, int rows) {
+    return moe_panels_offset(nt, deep) + rows * moe_row_bytes(tiles);
+}
+__host__ __device__ constexpr int moe_table_offset(int nt, bool deep, int tiles, int rows) {
+    return moe_flags_offset(nt, deep, tiles, rows) + kMoeMaxPanels * tiles * 4;
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
@@ -145,56 +148,53 @@ __device__ __forceinline__ void moe_scales(uint32_t w0, uint32_t w1, int c, floa
     s1 = __uint_as_float(r & 0xFFFF0000u);
 }
 
-// The plan's chunks, per expert ceil(rows / chunk_rows) of them in expert order, make `blocks` items each. Returns the item range
-// of CTA c of `ctas` and fills table[] with the chunks that it meets. Offsets are clamped into [0, R], so
-// rows of a malformed plan stay inside the workspace; they are read past L1. Called by the whole CTA.
-__device__ __forceinline__ void moe_find_items(const MoeArgs &a, int c, int ctas, int blocks, MoeChunk *table, int &begin,
-                                               int &end) {
-    __shared__ int32_t s_sum[kMoeWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int per = a.chunk_rows;
-    int32_t total = 0;
-    const int passes = a.E <= kMoeThreads ? 1 : 2;   // up to 512 experts one pass knows the total; else count first
+// The plan's chunks, per expert ceil(rows / chunk_rows) of them in expert order, make `blocks` items each. Returns the item
+// range of CTA c of `ctas` and the number of its first item in that item's chunk, and fills table[] with the chunks that
+// it meets. Offsets are clamped into [0, R], so rows of a malformed plan stay inside the workspace; they are read past
+// L1, once per CTA into `off_s` (all CTAs read the same few lines). Every warp scans them, with the same result.
+__device__ __forceinline__ void moe_find_items(const MoeArgs &a, int c, int ctas, int blocks, int32_t *off_s, MoeChunk *table,
+                                               int &begin, int &end, int &first) {
+    const int lane = threadIdx.x & 31, per = a.chunk_rows;
+    for (int e = threadIdx.x; e <= a.E; e += blockDim.x) off_s[e] = min(max(__ldcg(a.offsets + e), 0), a.R);
+    __syncthreads();
+    int total = 0;
+    const int passes = a.E <= 128 ? 1 : 2;   // up to 128 experts one pass knows the total; else count first
+#pragma unroll 1
     for (int pass = 0; pass < passes; ++pass) {
-        int32_t before = 0;
-        for (int base = 0; base < a.E; base += kMoeThreads) {
-            const int e = base + threadIdx.x;
-            int32_t lo = 0, rows = 0;
-            if (e < a.E) {
-                lo = min(max(__ldcg(a.offsets + e), 0), a.R);
-                rows = max(min(max(__ldcg(a.offsets + e + 1), 0), a.R) - lo, 0);
-            }
-            const int32_t n = (rows + per - 1) / per;
+        int before = 0;
+#pragma unroll 1
+        for (int base = 0; base < a.E; base += 128) {
+            int32_t off[5], n = 0;
+#pragma unroll
+            for (int i = 0; i < 5; ++i) off[i] = off_s[min(base + 4 * lane + i, a.E)];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) n += (max(off[i + 1] - off[i], 0) + per - 1) / per;
             int32_t x = n;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int32_t y = __shfl_up_sync(0xffffffffu, x, d);
                 if (lane >= d) x += y;
             }
-            __syncthreads();
-            if (lane == 31) s_sum[warp] = x;
-            __syncthreads();
             int32_t at = before + x - n;
-#pragma unroll
-            for (int w = 0; w < kMoeWarps; ++w) {
-                const int32_t v = s_sum[w];
-                at += w < warp ? v : 0;
-                before += v;
-            }
-            if (pass == 0) total = before;
+            before += __shfl_sync(0xffffffffu, x, 31);
+            if (pass == 0) total = min(before, 60000);   // a sound plan has fewer; keeps item numbers in 31 bits
             if (pass == passes - 1) {
-                const int64_t items = static_cast<int64_t>(total) * blocks;
-                begin = static_cast<int>(items * c / ctas);
-                end = static_cast<int>(items * (c + 1) / ctas);
+                const int items = total * blocks, share = items / ctas, rest = items - share * ctas;
+                begin = c * share + min(c, rest);
+                end = begin + share + (c < rest ? 1 : 0);
                 const int z0 = begin / blocks;
+                first = begin - z0 * blocks;
                 end = min(end, (z0 + a.max_chunks) * blocks);   // more only where a plan lists a row twice
                 const int z1 = begin < end ? (end - 1) / blocks : -1;
-                for (int z = max(z0, at); z < at + n && z <= z1; ++z)
-                    table[z - z0] = {e, lo + (z - at) * per, min(rows - (z - at) * per, per)};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    for (int rows = off[i + 1] - off[i]; rows > 0; rows -= per, ++at)
+                        if (at >= z0 && at <= z1)
+                            table[at - z0] = {base + 4 * lane + i, off[i + 1] - rows, min(rows, per)};
             }
         }
     }
-    __syncthreads();
+    __syncthreads();   // off_s is free again
 }
 
 // log2 of the power of two s that a group is scaled by before fp16, from its largest magnitude: 0 when that is in
@@ -253,82 +253,107 @@ __device__ __forceinline__ void moe_tile_mma(uint32_t codes, const uint32_t (&wo
     }
 }
 
-// One 32-channel group per thread, 16 packed pairs: multipliers, the block Hadamard of order kB, fp16 into the panel. For
-// kB > 32 the neighbouring lanes hold the neighbouring groups; the whole warp calls it. Returns 1 / s.
-template <int kB>
-__device__ __forceinline__ float moe_group_to_half(uint64_t (&p)[16], const float *mul, bool on, uint8_t *dst) {
-    if (mul != nullptr) {
-        uint64_t mv[16];
-        load_mul(mul, mv);
+// Eight neighbouring channels of a panel row per lane, 16 lanes a 128-channel block: the block Hadamard of order b (stages h = 1, 2, ... in order), fp16. Returns 1 / s of the lane's group. The whole warp calls it.
+__device__ __forceinline__ float moe_to_half(float (&v)[8], int b, uint4 &out) {
+    if (b > 1) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) p[i] = mul2(p[i], mv[i]);
+        for (int h = 1; h < 8; h <<= 1)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if ((i & h) == 0) {
+                    const float p = v[i], q = v[i + h];
+                    v[i] = p + q;
+                    v[i + h] = p - q;
+                }
+#pragma unroll 1
+        for (int d = 1; 8 * d < b; d <<= 1) {   // stage h = 8 d
+            const float sign = (threadIdx.x & d) ? -1.0f : 1.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = fmaf(v[i], sign, __shfl_xor_sync(0xffffffffu, v[i], d));
+        }
     }
-    fwht_in_thread<kB>(p);
-    if constexpr (kB >= 64) fwht_cross_lane(p, 1);
-    if constexpr (kB >= 128) fwht_cross_lane(p, 2);
     float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        float a, b;
-        upk2(p[i], a, b);
-        top = fmaxf(top, fmaxf(fabsf(a), fabsf(b)));
-    }
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[i]));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const int shift = moe_shift(top);
     const float s = moe_pow2(shift);
-    const uint64_t s2 = pk2(s, s);
-    uint32_t h[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        float a, b;
-        upk2(mul2(p[i], s2), a, b);
-        h[i] = half2_bits(a, b);
-    }
-    if (on)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4 *>(dst + 16 * i) = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+    out = make_uint4(half2_bits(v[0] * s, v[1] * s), half2_bits(v[2] * s, v[3] * s), half2_bits(v[4] * s, v[5] * s),
+                     half2_bits(v[6] * s, v[7] * s));
     return moe_pow2(-shift);
 }
 
-// The panel rows of a phase from X (kernel 1) or from h (kernel 2): `total` groups, row by row. rows: per panel row the chunk
-// (its number in the phase) and the row of X or h.
+// The panel rows of a phase from X (kernel 1) or from h (kernel 2). rows: per panel row the chunk (its number in the
+// phase) and the row of X or h.
 struct MoeRow {
     int32_t panel, source;
 };
 
-template <int kB, bool kDown>
+// after_loads() runs once the first loads are on their way.
+template <bool kDown, int kThreads, typename AfterLoads>
 __device__ __forceinline__ void moe_fill_panels(const MoeArgs &a, const MoeChunk *chunks, const MoeRow *rows, int count, uint8_t *panel,
-                                                float *xs, int32_t *flags) {
-    const int width = kDown ? a.I : a.K, groups = width / 32, total = count * groups, lane = threadIdx.x & 31;
+                                                float *xs, int32_t *flags, AfterLoads after_loads) {
+    const int width = kDown ? a.I : a.K, units = width / 8, total = count * units, lane = threadIdx.x & 31;
     const int stride = moe_panel_stride(width / 128);
     const float *inv_s = kDown ? a.inv_dn : a.inv_gu;
+    constexpr int kAtOnce = 2;   // units whose loads are in flight
+    bool first = true;
 #pragma unroll 1
-    for (int base = threadIdx.x & ~31; base < total; base += kMoeThreads) {
-        const int u = min(base + lane, total - 1);
-        const int row = u / groups, gr = u - row * groups;
-        const MoeRow r = rows[row];
-        const int64_t k = gr * 32;
-        uint64_t p[16];
-        if constexpr (kDown) {
-            const float4 *src = reinterpret_cast<const float4 *>(a.h + static_cast<int64_t>(r.source) * a.I + k);
+    for (int base = threadIdx.x & ~31; base < total; base += kAtOnce * kThreads) {
+        float4 f[kAtOnce][2], m[kAtOnce][2];
+        int row[kAtOnce], c[kAtOnce], chunk[kAtOnce];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float4 f = __ldcg(src + i);
-                p[2 * i] = pk2(f.x, f.y);
-                p[2 * i + 1] = pk2(f.z, f.w);
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int u = min(base + k * kThreads + lane, total - 1);
+            row[k] = u / units;
+            c[k] = u - row[k] * units;
+            const MoeRow r = rows[row[k]];
+            chunk[k] = r.panel;
+            if constexpr (kDown) {
+                const float4 *src = reinterpret_cast<const float4 *>(a.h + static_cast<int64_t>(r.source) * a.I + 8 * c[k]);
+                f[k][0] = __ldcg(src), f[k][1] = __ldcg(src + 1);
+            } else {
+                f[k][0] = __ldcg(reinterpret_cast<const float4 *>(a.x + static_cast<int64_t>(r.source) * a.K + 8 * c[k]));
             }
-        } else {
-            uint4 raw[4];
-            load_group_global(a.x + static_cast<int64_t>(r.source) * a.K + k, raw);
-            unpack_bf16x32(raw, p);
+            m[k][0] = m[k][1] = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+            if (inv_s != nullptr) {
+                const float4 *mul = reinterpret_cast<const float4 *>(inv_s + static_cast<int64_t>(chunks[r.panel].e) * width + 8 * c[k]);
+                m[k][0] = __ldg(mul), m[k][1] = __ldg(mul + 1);
+            }
         }
-        const float *mul = inv_s == nullptr ? nullptr : inv_s + static_cast<int64_t>(chunks[r.panel].e) * width + k;
-        const float inv = moe_group_to_half<kB>(p, mul, base + lane < total, panel + row * stride + gr * 64);
-        if (base + lane < total) {
-            xs[u] = inv;
-            if (inv != 1.0f) flags[r.panel * (width / 128) + (gr >> 2)] = 1;
+        if (first) after_loads();
+        first = false;
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            if (base + k * kThreads >= total) break;
+            float v[8];
+            if constexpr (kDown) {
+                v[0] = f[k][0].x, v[1] = f[k][0].y, v[2] = f[k][0].z, v[3] = f[k][0].w;
+                v[4] = f[k][1].x, v[5] = f[k][1].y, v[6] = f[k][1].z, v[7] = f[k][1].w;
+            } else {
+                const uint32_t w[4] = {__float_as_uint(f[k][0].x), __float_as_uint(f[k][0].y), __float_as_uint(f[k][0].z),
+                                       __float_as_uint(f[k][0].w)};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[2 * i] = __uint_as_float(w[i] << 16);
+                    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+                }
+            }
+            v[0] *= m[k][0].x, v[1] *= m[k][0].y, v[2] *= m[k][0].z, v[3] *= m[k][0].w;
+            v[4] *= m[k][1].x, v[5] *= m[k][1].y, v[6] *= m[k][1].z, v[7] *= m[k][1].w;
+            uint4 h;
+            const float inv = moe_to_half(v, kDown ? a.b_dn : a.b_gu, h);
+            if (base + k * kThreads + lane < total) {
+                *reinterpret_cast<uint4 *>(panel + row[k] * stride + c[k] * 16) = h;
+                if ((lane & 3) == 0) {
+                    xs[row[k] * (width / 32) + c[k] / 4] = inv;
+                    if (inv != 1.0f) flags[chunk[k] * (width / 128) + c[k] / 16] = 1;
+                }
+            }
         }
     }
+    if (first) after_loads();
 }
 
 // The weight stream of one warp: the K tiles of consecutive items. issue() starts the copies of the next tile.
@@ -405,19 +430,20 @@ __device__ __forceinline__ void moe_store_item(const MoeArgs &a, const MoeChunk 
 // ahead of it, so that the instructions are cached when the operands arrive; what that pass computes is dropped. Measured
 // for one token of 128 experts, top-8, 2048 x 768: the first tile after the wait took 2.2 us without the pass.
 template <bool kDown, int kNt, bool kDeep>
-__global__ void __launch_bounds__(kMoeThreads, 2) moe_w4a16_kernel(MoeArgs a) {
-    constexpr int kStages = kDeep ? kMoeDeepStages : kMoeWideStages;
+__global__ void __launch_bounds__(32 * (kDeep ? kMoeDeepWarps : kMoeWideWarps), kDeep ? 2 : 1) moe_w4a16_kernel(MoeArgs a) {
+    constexpr int kStages = kDeep ? kMoeDeepStages : kMoeWideStages, kWarps = kDeep ? kMoeDeepWarps : kMoeWideWarps;
+    constexpr int kThreads = 32 * kWarps;
     extern __shared__ __align__(128) uint8_t s_raw[];
     __shared__ MoeRow s_rows[kMoeMaxPanels * 8 * kNt];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     if constexpr (kDown) griddep_launch_dependents();
 
     const int kt = (kDown ? a.I : a.K) / 128, stride = moe_panel_stride(kt);
-    float *heads = reinterpret_cast<float *>(s_raw + moe_heads_offset(kStages));
-    uint8_t *panel = s_raw + moe_panels_offset(kNt, kStages);
+    float *heads = reinterpret_cast<float *>(s_raw + moe_heads_offset(kDeep));
+    uint8_t *panel = s_raw + moe_panels_offset(kNt, kDeep);
     float *xs = reinterpret_cast<float *>(panel + a.panel_rows * stride);   // [row][group]
-    int32_t *flags = reinterpret_cast<int32_t *>(s_raw + moe_flags_offset(kNt, kStages, kt, a.panel_rows));
-    MoeChunk *table = reinterpret_cast<MoeChunk *>(s_raw + moe_table_offset(kNt, kStages, kt, a.panel_rows));
+    int32_t *flags = reinterpret_cast<int32_t *>(s_raw + moe_flags_offset(kNt, kDeep, kt, a.panel_rows));
+    MoeChunk *table = reinterpret_cast<MoeChunk *>(s_raw + moe_table_offset(kNt, kDeep, kt, a.panel_rows));
 
     MoeStream<kStages> w;
     w.wq = kDown ? a.wq_dn : a.wq_gu;
@@ -442,12 +468,11 @@ __global__ void __launch_bounds__(kMoeThreads, 2) moe_w4a16_kernel(MoeArgs a) {
                 griddep_wait();
                 griddep_launch_dependents();
             }
-            moe_find_items(a, blockIdx.x, gridDim.x, w.per_chunk, table, begin, end);
+            moe_find_items(a, blockIdx.x, gridDim.x, w.per_chunk, reinterpret_cast<int32_t *>(panel), table, begin, end, r);
             from = begin;
-            r = begin % w.per_chunk;
             found = true;
         }
-        auto cut = [&](int i) { return static_cast<int>(static_cast<int64_t>(total) * i / kMoeWarps); };
+        auto cut = [&](int i) { return static_cast<int>(static_cast<int64_t>(total) * i / kWarps); };
         if (found && !prepared) {
             if (from >= end) break;
             // a phase: the items of as many chunks as have their panel rows in shared memory at a time
@@ -460,12 +485,12 @@ __global__ void __launch_bounds__(kMoeThreads, 2) moe_w4a16_kernel(MoeArgs a) {
             }
             total = (to - from) * kt;
             first = cut(warp), last = cut(warp + 1);
-            tile = first % kt;   // where this warp starts
-            item_r = r + first / kt;
-            item_z = z + item_r / w.per_chunk;
-            item_r %= w.per_chunk;
-            w.start(item_z, item_r, tile, last - first);
-            for (int i = threadIdx.x; i < chunks * 8 * kNt; i += kMoeThreads) {
+            item_r = first / kt;   // where this warp starts
+            tile = first - item_r * kt;
+            item_r += r;
+            for (item_z = z; item_r >= w.per_chunk; item_r -= w.per_chunk) ++item_z;
+            if constexpr (kDown) w.start(item_z, item_r, tile, last - first);
+            for (int i = threadIdx.x; i < chunks * 8 * kNt; i += kThreads) {
                 int at = i % (8 * kNt);
                 const MoeChunk ch = table[z + i / (8 * kNt)];
                 if (at >= ch.rows) continue;
@@ -479,18 +504,14 @@ __global__ void __launch_bounds__(kMoeThreads, 2) moe_w4a16_kernel(MoeArgs a) {
             table[0] = {0, 0, 1};
             s_rows[0] = {0, 0};
         }
-        for (int i = threadIdx.x; i < chunks * kt; i += kMoeThreads) flags[i] = 0;
+        for (int i = threadIdx.x; i < chunks * kt; i += kThreads) flags[i] = 0;
         if constexpr (kDown)
             if (!dry && from == begin) griddep_wait();
         __syncthreads();
-        const int fill = dry ? 1 : rows;
-        switch (kDown ? a.b_dn : a.b_gu) {
-            case 1: moe_fill_panels<1, kDown>(a, table + z, s_rows, fill, panel, xs, flags); break;
-            case 16: moe_fill_panels<16, kDown>(a, table + z, s_rows, fill, panel, xs, flags); break;
-            case 32: moe_fill_panels<32, kDown>(a, table + z, s_rows, fill, panel, xs, flags); break;
-            case 64: moe_fill_panels<64, kDown>(a, table + z, s_rows, fill, panel, xs, flags); break;
-            default: moe_fill_panels<128, kDown>(a, table + z, s_rows, fill, panel, xs, flags); break;
-        }
+        // kernel 1 has its operands on their way before the weights queue up behind them
+        moe_fill_panels<kDown, kThreads>(a, table + z, s_rows, dry ? 1 : rows, panel, xs, flags, [&] {
+            if (!kDown && !dry) w.start(item_z, item_r, tile, last - first);
+        });
         __syncthreads();
 
         float acc[2][kNt][4] = {};
@@ -565,21 +586,27 @@ __global__ void __launch_bounds__(kMoeThreads, 2) moe_w4a16_kernel(MoeArgs a) {
         }
         __syncthreads();
         // a cut item is closed by the first warp that starts inside it: the piece before, its own, and those after
-        if (first % kt != 0 && warp > 0 && cut(warp - 1) <= first / kt * kt) {
-            const int stop = (first / kt + 1) * kt;
+        const int whole_items = first / kt;
+        if (first != whole_items * kt && warp > 0 && cut(warp - 1) <= whole_items * kt) {
+            const int stop = (whole_items + 1) * kt;
             const float *before = reinterpret_cast<const float *>(s_raw + (warp - 1) * kStages * kMoeStageBytes);
 #pragma unroll
             for (int i = 0; i < 8 * kNt; ++i) acc[i / (4 * kNt)][i / 4 % kNt][i % 4] = before[i * 32 + lane];
-            for (int v = warp; v < kMoeWarps && cut(v) < stop; ++v) {
+            for (int v = warp; v < kWarps && cut(v) < stop; ++v) {
                 if (cut(v) == cut(v + 1)) continue;
 #pragma unroll
                 for (int i = 0; i < 8 * kNt; ++i) acc[i / (4 * kNt)][i / 4 % kNt][i % 4] += heads[(v * 8 * kNt + i) * 32 + lane];
             }
-            const int it = r + first / kt;
-            moe_store_item<kDown, kNt>(a, table[z + it / w.per_chunk], it % w.per_chunk, acc, lane);
+            int it = r + whole_items, iz = z;
+            for (; it >= w.per_chunk; it -= w.per_chunk) ++iz;
+            moe_store_item<kDown, kNt>(a, table[iz], it, acc, lane);
         }
-        r = (r + to - from) % w.per_chunk;
-        z += r == 0 ? chunks : chunks - 1;
+        r += to - from - (chunks - 1) * w.per_chunk;   // in the phase's last chunk
+        z += chunks - 1;
+        if (r == w.per_chunk) {
+            r = 0;
+            ++z;
+        }
         from = to;
         prepared = false;
         __syncthreads();   // panels and pieces are read before the next phase writes them
