@@ -2,8 +2,19 @@
 //
 //   out[m, :] = Y[m, :] + scale[a] * (X[m, :] A[a]^T) B[a]^T     for the rows m of adapter a
 //
-// Rows come sorted by adapter through group_offsets and row_index (a row plan); rows of no adapter are copied when
-// out is not Y. X A^T is held in fp32.
+// Bound by HBM: for a prefill by Y in and out, for a decode batch by the active adapters' A and B; for a few rows by latency.
+//
+// One launch. A cluster of eight CTAs takes a chunk of up to 16 or 64 rows of one adapter (rows of no adapter are chunks of
+// their own, copied when out is not Y). Each CTA computes the chunk's V = X A^T over an eighth of K; the partial sums are
+// added through distributed shared memory (each CTA adds an eighth of V and sends it to all), and each CTA then adds
+// V B^T to an eighth of the columns. A and B are read once per chunk, V never leaves the chip, and while the first product
+// runs the CTA's part of B is already on its way into L2.
+//
+// Both products are bf16 MMAs (m16n8k16) fed straight from global memory: lane (g, t) takes 16 bytes, 8 neighbouring k of
+// row g at 8 t of a 32-wide k step, and the two MMAs of the step take their halves; both operands use the same order, so
+// the sum over k is complete. In the second product the 32 columns of a step are dealt to the four n8 tiles so that a lane
+// ends up with 8 neighbouring columns of a row: Y moves in 16-byte pieces. V is held as two bf16 parts (16 bits) for
+// bf16 outputs and three (24 bits, all of fp32) for fp32, so it is not what limits the result.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -15,6 +26,8 @@
 namespace macaq {
 
 constexpr int kLoraThreads = 256;
+constexpr int kLoraWarps = kLoraThreads / 32;
+constexpr int kLoraCluster = 8;
 constexpr int kLoraMaxRank = 128;
 
 struct LoraArgs {
@@ -30,44 +43,284 @@ struct LoraArgs {
     int32_t r, L, f32;
 };
 
-__device__ __forceinline__ float bf16_value(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+// Shared memory for rank r (rounded up to 32 in the parts of V), chunks of 16 mt rows and `parts` bf16 parts of V: the CTA's
+// partial V per k split, its sum, the parts of V.
+__host__ __device__ constexpr int lora_rank32(int r) { return (r + 31) / 32 * 32; }
+__host__ __device__ constexpr int lora_v_stride(int r) { return lora_rank32(r) + 8; }   // bf16: rows 16 bytes off a multiple of 64
+__host__ __device__ constexpr int lora_splits(int mt) { return kLoraWarps / mt; }
+__host__ __device__ constexpr int lora_smem_bytes(int r, int mt, int parts) {
+    return (lora_splits(mt) + 1) * 16 * mt * r * 4 + parts * 16 * mt * lora_v_stride(r) * 2;
+}
 
-__global__ void __launch_bounds__(kLoraThreads) lora_add_kernel(LoraArgs p) {
-    __shared__ float s_v[kLoraMaxRank];
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint4 lora_ld(const uint16_t *p, bool on) {
+    return on ? __ldg(reinterpret_cast<const uint4 *>(p)) : make_uint4(0u, 0u, 0u, 0u);
+}
+
+struct LoraChunk {
+    int32_t a, rows;   // adapter (L: rows of no adapter), rows; rows = 0: there is no such chunk
+    int64_t row0;
+};
+
+// Chunk z of the plan: ceil(rows / most) of them per adapter, the rows of none as one more group at the end. Offsets are
+// clamped into [0, M]. Every warp finds the same; s_off holds the offsets.
+__device__ __forceinline__ LoraChunk lora_find_chunk(const LoraArgs &p, int z, int most, int32_t *s_off) {
+    const int lane = threadIdx.x & 31;
+    for (int i = threadIdx.x; i <= p.L; i += kLoraThreads)
+        s_off[i] = static_cast<int32_t>(min(max(static_cast<int64_t>(__ldcg(p.offsets + i)), int64_t{0}), p.M));
+    if (threadIdx.x == 0) s_off[p.L + 1] = static_cast<int32_t>(p.M);
+    __syncthreads();
+    LoraChunk ch{0, 0, 0};
+    int64_t before = 0;
+#pragma unroll 1
+    for (int base = 0; base <= p.L; base += 32) {
+        const int g = base + lane;
+        const int32_t lo = g <= p.L ? s_off[g] : 0, rows = g <= p.L ? max(s_off[g + 1] - lo, 0) : 0;
+        const int32_t n = (rows + most - 1) / most;
+        int32_t x = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int32_t y = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += y;
+        }
+        const int64_t at = before + x - n;
+        const uint32_t hit = __ballot_sync(0xffffffffu, z >= at && z < at + n);
+        if (hit != 0) {
+            const int src = __ffs(hit) - 1;
+            const int32_t skip = static_cast<int32_t>(z - __shfl_sync(0xffffffffu, at, src)) * most;
+            ch.a = base + src;
+            ch.row0 = static_cast<int64_t>(__shfl_sync(0xffffffffu, lo, src)) + skip;
+            ch.rows = min(__shfl_sync(0xffffffffu, rows, src) - skip, most);
+            break;
+        }
+        before += __shfl_sync(0xffffffffu, x, 31);
+    }
+    return ch;
+}
+
+// Eight neighbouring outputs of a row: out = y + d.
+template <bool kF32>
+struct LoraPiece {
+    uint4 v[kF32 ? 2 : 1];
+    __device__ __forceinline__ void load(const void *y, int64_t at, bool on) {
+        if (!on) return;
+        if constexpr (kF32) {
+            const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(y) + at);
+            v[0] = __ldcg(p), v[1] = __ldcg(p + 1);
+        } else {
+            v[0] = __ldcg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(y) + at));
+        }
+    }
+    __device__ __forceinline__ void add(const float (&d)[8]) {
+        if constexpr (kF32) {
+            uint32_t *w = reinterpret_cast<uint32_t *>(v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) + d[i]);
+        } else {
+            uint32_t *w = reinterpret_cast<uint32_t *>(v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(w[i] << 16) + d[2 * i],
+                                                               __uint_as_float(w[i] & 0xFFFF0000u) + d[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t *>(&b);
+            }
+        }
+    }
+    __device__ __forceinline__ void store(void *out, int64_t at, bool on) const {
+        if (!on) return;
+        if constexpr (kF32) {
+            uint4 *p = reinterpret_cast<uint4 *>(static_cast<float *>(out) + at);
+            p[0] = v[0], p[1] = v[1];
+        } else {
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + at) = v[0];
+        }
+    }
+};
+
+// Grid: one cluster per chunk. kMt: m16 tiles of a chunk.
+template <int kMt, bool kF32>
+__global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
+    constexpr int kRows = 16 * kMt, kSplits = lora_splits(kMt), kParts = kF32 ? 3 : 2;
+    extern __shared__ __align__(16) uint8_t s_lora[];
+    __shared__ int32_t s_off[kRouteMaxExperts + 2];
+    __shared__ int64_t s_row[kRows];   // row of X, Y and out, -1: none
     griddep_wait();
     griddep_launch_dependents();
-    const int64_t s = blockIdx.x;
-    int a = -1;
-    int64_t lo = 0;
-    for (int g = 0; g < p.L; ++g) {
-        int64_t hi = p.offsets[g + 1];
-        hi = hi < lo ? lo : (hi > p.M ? p.M : hi);
-        if (s >= lo && s < hi) a = g;
-        lo = hi;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int rank = blockIdx.x % kLoraCluster;
+    const LoraChunk ch = lora_find_chunk(p, blockIdx.x / kLoraCluster, kRows, s_off);
+    if (ch.rows == 0 || (ch.a == p.L && p.out == p.y)) return;   // the same for the whole cluster
+    const int r = p.r;
+    // this CTA's columns, in steps of 32, and k steps of 32
+    const int64_t nsteps = (p.N + 31) / 32, n_begin = nsteps * rank / kLoraCluster, n_end = nsteps * (rank + 1) / kLoraCluster;
+    const int64_t ksteps = (p.K + 31) / 32, k_begin = ksteps * rank / kLoraCluster, k_end = ksteps * (rank + 1) / kLoraCluster;
+    for (int i = threadIdx.x; i < kRows; i += kLoraThreads) {
+        int64_t m = -1;
+        if (i < ch.rows) m = p.row_index ? static_cast<int64_t>(__ldcg(p.row_index + ch.row0 + i)) : ch.row0 + i;
+        s_row[i] = m >= 0 && m < p.M ? m : -1;
     }
-    const int64_t m = p.row_index ? p.row_index[s] : s;
-    if (m < 0 || m >= p.M || (a < 0 && p.out == p.y)) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (a >= 0)
-        for (int j = warp; j < p.r; j += kLoraThreads / 32) {
-            const uint16_t *row = p.A + (static_cast<int64_t>(a) * p.r + j) * p.K;
-            float v = 0.0f;
-            for (int64_t k = lane; k < p.K; k += 32) v = fmaf(bf16_value(p.x[m * p.ldx + k]), bf16_value(row[k]), v);
-            v = warp_sum(v);
-            if (lane == 0) s_v[j] = p.scale ? v * p.scale[a] : v;
-        }
     __syncthreads();
-    for (int64_t n = threadIdx.x; n < p.N; n += kLoraThreads) {
-        float v = p.f32 ? static_cast<const float *>(p.y)[m * p.ldy + n]
-                        : bf16_value(static_cast<const uint16_t *>(p.y)[m * p.ldy + n]);
-        if (a >= 0) {
-            const uint16_t *row = p.B + (static_cast<int64_t>(a) * p.N + n) * p.r;
-            float d = 0.0f;
-            for (int j = 0; j < p.r; ++j) d = fmaf(s_v[j], bf16_value(row[j]), d);
-            v += d;
+
+    if (ch.a == p.L) {   // rows of no adapter
+        const int64_t per = (n_end - n_begin) * 4;
+        for (int64_t i = threadIdx.x; i < ch.rows * per; i += kLoraThreads) {
+            const int64_t m = s_row[i / per], n = n_begin * 32 + i % per * 8;
+            LoraPiece<kF32> y;
+            y.load(p.y, m * p.ldy + n, m >= 0 && n < p.N);
+            y.store(p.out, m * p.ldo + n, m >= 0 && n < p.N);
         }
-        if (p.f32) static_cast<float *>(p.out)[m * p.ldo + n] = v;
-        else static_cast<__nv_bfloat16 *>(p.out)[m * p.ldo + n] = __float2bfloat16_rn(v);
+        return;
+    }
+
+    const uint16_t *A = p.A + static_cast<int64_t>(ch.a) * r * p.K, *B = p.B + static_cast<int64_t>(ch.a) * p.N * r;
+    {   // this CTA's part of B, towards L2
+        const char *from = reinterpret_cast<const char *>(B + n_begin * 32 * r);
+        const int64_t bytes = (min(n_end * 32, p.N) - n_begin * 32) * r * 2;
+        for (int64_t i = threadIdx.x * 128; i < bytes; i += kLoraThreads * 128)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(from + i));
+    }
+
+    // V = X A^T: a warp takes one m16 tile and every kSplits-th k step of the CTA's part
+    float *part = reinterpret_cast<float *>(s_lora), *mine = part + kSplits * kRows * r;   // [split][row][r], [row][r]
+    uint16_t *v_s = reinterpret_cast<uint16_t *>(mine + kRows * r);                       // [part][row][stride]
+    const int vs = lora_v_stride(r);
+    {
+        const int mt = warp % kMt, split = warp / kMt;
+        const int64_t row_lo = s_row[16 * mt + g], row_hi = s_row[16 * mt + g + 8];
+        const uint16_t *x_lo = p.x + row_lo * p.ldx + 8 * t, *x_hi = p.x + row_hi * p.ldx + 8 * t;
+        constexpr int kTiles = 4;   // n8 tiles of V at a time
+        for (int j0 = 0; j0 < r; j0 += 8 * kTiles) {
+            float acc[kTiles][4] = {};
+#pragma unroll 2
+            for (int64_t s = k_begin + split; s < k_end; s += kSplits) {
+                const int64_t k = s * 32;
+                const bool on = k + 8 * t < p.K;
+                const uint4 lo = lora_ld(x_lo + k, on && row_lo >= 0), hi = lora_ld(x_hi + k, on && row_hi >= 0);
+                uint4 b[kTiles];
+#pragma unroll
+                for (int j = 0; j < kTiles; ++j)
+                    b[j] = lora_ld(A + static_cast<int64_t>(j0 + 8 * j + g) * p.K + k + 8 * t, on && j0 + 8 * j < r);
+#pragma unroll
+                for (int j = 0; j < kTiles; ++j) {
+                    mma_bf16(acc[j], lo.x, hi.x, lo.y, hi.y, b[j].x, b[j].y);
+                    mma_bf16(acc[j], lo.z, hi.z, lo.w, hi.w, b[j].z, b[j].w);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j)
+                if (j0 + 8 * j < r) {
+                    float *dst = part + (split * kRows + 16 * mt + g) * r + j0 + 8 * j + 2 * t;
+                    *reinterpret_cast<float2 *>(dst) = make_float2(acc[j][0], acc[j][1]);
+                    *reinterpret_cast<float2 *>(dst + 8 * r) = make_float2(acc[j][2], acc[j][3]);
+                }
+        }
+    }
+    // the parts' columns from r to the next multiple of 32 are zero
+    for (int i = threadIdx.x; i < kParts * kRows * (lora_rank32(r) - r); i += kLoraThreads) {
+        const int per = lora_rank32(r) - r;
+        v_s[i / per * vs + r + i % per] = 0;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < kRows * r; i += kLoraThreads) {
+        float v = 0.0f;
+#pragma unroll
+        for (int s = 0; s < kSplits; ++s) v += part[s * kRows * r + i];
+        mine[i] = v;
+    }
+    cluster_sync();
+    {   // entries in pairs, an eighth of them per CTA: sum over the cluster, times scale, to everybody in bf16 parts
+        const float scale = p.scale ? __ldg(p.scale + ch.a) : 1.0f;
+        const int pairs = kRows * r / 2;
+        for (int i = rank * pairs / kLoraCluster + threadIdx.x; i < (rank + 1) * pairs / kLoraCluster; i += kLoraThreads) {
+            float v0 = 0.0f, v1 = 0.0f;
+#pragma unroll
+            for (int c = 0; c < kLoraCluster; ++c) {
+                float a0, a1;
+                asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                             : "=f"(a0), "=f"(a1)
+                             : "r"(map_to_rank(smem_u32(mine + 2 * i), c))
+                             : "memory");
+                v0 += a0, v1 += a1;
+            }
+            v0 *= scale, v1 *= scale;
+            const int row = 2 * i / r, col = 2 * i - row * r;
+#pragma unroll
+            for (int k = 0; k < kParts; ++k) {   // each part is the rounding of what the ones before leave
+                const __nv_bfloat162 b = __floats2bfloat162_rn(v0, v1);
+                const uint32_t w = *reinterpret_cast<const uint32_t *>(&b);
+                v0 -= __uint_as_float(w << 16), v1 -= __uint_as_float(w & 0xFFFF0000u);
+#pragma unroll
+                for (int c = 0; c < kLoraCluster; ++c)
+                    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
+                                     map_to_rank(smem_u32(v_s + (k * kRows + row) * vs + col), c)),
+                                 "r"(w)
+                                 : "memory");
+            }
+        }
+    }
+    __syncwarp();
+    cluster_sync();
+
+    // out = Y + V B^T: a warp takes every eighth 32-column step for all rows. Logical column c of n8 tile i is column
+    // 8 (c / 2) + 2 i + c % 2 of the step.
+    const int steps = lora_rank32(r) / 32;
+    constexpr int kPair = kMt < 2 ? 1 : 2;   // m16 tiles at a time: their sums and pieces of Y fit in registers
+    for (int64_t s = n_begin + warp; s < n_end; s += kLoraWarps) {
+        const int64_t n0 = s * 32;
+        const bool on = n0 + 8 * t < p.N;
+#pragma unroll 1
+        for (int m0 = 0; m0 < kMt; m0 += kPair) {
+            if (16 * m0 >= ch.rows) break;
+            LoraPiece<kF32> y[kPair][2];
+#pragma unroll
+            for (int mt = 0; mt < kPair; ++mt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int64_t m = s_row[16 * (m0 + mt) + 8 * h + g];
+                    y[mt][h].load(p.y, m * p.ldy + n0 + 8 * t, on && m >= 0);
+                }
+            float acc[kPair][4][4] = {};
+#pragma unroll 1
+            for (int ks = 0; ks < steps; ++ks) {
+                const int k = ks * 32 + 8 * t;
+                uint4 b[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int64_t n = n0 + 8 * (g >> 1) + 2 * i + (g & 1);
+                    b[i] = lora_ld(B + n * r + k, n < p.N && k < r);
+                }
+#pragma unroll
+                for (int mt = 0; mt < kPair; ++mt)
+#pragma unroll
+                    for (int q = 0; q < kParts; ++q) {
+                        const uint16_t *v = v_s + (q * kRows + 16 * (m0 + mt) + g) * vs + k;
+                        const uint4 lo = *reinterpret_cast<const uint4 *>(v), hi = *reinterpret_cast<const uint4 *>(v + 8 * vs);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            mma_bf16(acc[mt][i], lo.x, hi.x, lo.y, hi.y, b[i].x, b[i].y);
+                            mma_bf16(acc[mt][i], lo.z, hi.z, lo.w, hi.w, b[i].z, b[i].w);
+                        }
+                    }
+            }
+#pragma unroll
+            for (int mt = 0; mt < kPair; ++mt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float d[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) d[2 * i] = acc[mt][i][2 * h], d[2 * i + 1] = acc[mt][i][2 * h + 1];
+                    const int64_t m = s_row[16 * (m0 + mt) + 8 * h + g];
+                    y[mt][h].add(d);
+                    y[mt][h].store(p.out, m * p.ldo + n0 + 8 * t, on && m >= 0);
+                }
+        }
     }
 }
 

@@ -1135,39 +1135,32 @@ bool moe_w4a16_shape_ok(int64_t T, int32_t topk, int32_t E, int64_t K, int64_t I
 }
 
 // Kernel 1 or 2, with column tiles for 8 kNt rows.
-template <bool kDown, int kNt, bool kDeep>
+template <bool kDown, int kNt>
 macaq_status moe_launch(MoeArgs g, int sms, cudaStream_t st) {
-    // shared memory of a CTA: an SM's, or half, less the static arrays and the runtime's share
-    constexpr int kSmem = (kDeep ? 116224 : 232448) - 4 * 1024;
+    constexpr int kSmem = 232448 - 4 * 1024;   // of an SM, less the static arrays
     constexpr int kTable = 1024;   // room for the chunk table: a CTA meets a few chunks
     const int tiles = (kDown ? g.I : g.K) / 128;
     const int64_t per_chunk = (kDown ? g.N : 2 * g.I) / 32;
     // panel rows: what fits; a chunk has no more rows than that
-    const int fixed = moe_table_offset(kNt, kDeep, tiles, 0) + kTable;
+    const int fixed = moe_table_offset(kNt, tiles, 0) + kTable;
     g.panel_rows = std::min((kSmem - fixed) / moe_row_bytes(tiles), kMoeMaxPanels * 8 * kNt);
-    if constexpr (kDeep)
-        if (g.panel_rows < (kNt == 1 ? 4 : 24)) return moe_launch<kDown, kNt, false>(g, sms, st);   // would take phases
     if (g.panel_rows < 1) return MACAQ_ERR_SHAPE;
     g.chunk_rows = std::min(8 * kNt, g.panel_rows);
     const int64_t chunks = std::min(g.E, g.R) + g.R / g.chunk_rows, items = chunks * per_chunk;
     const int64_t ctas = std::min<int64_t>(items, sms);
     g.max_chunks = static_cast<int32_t>((items + ctas - 1) / ctas / per_chunk + 2);
-    const size_t smem = moe_table_offset(kNt, kDeep, tiles, g.panel_rows) + g.max_chunks * sizeof(MoeChunk);
+    const size_t smem = moe_table_offset(kNt, tiles, g.panel_rows) + g.max_chunks * sizeof(MoeChunk);
     if (smem > kSmem) return MACAQ_ERR_SHAPE;
-    auto k = moe_w4a16_kernel<kDown, kNt, kDeep>;
+    auto k = moe_w4a16_kernel<kDown, kNt>;
     macaq_status s = set_smem(k, smem);
     if (s != MACAQ_OK) return s;
-    return launch(k, dim3(static_cast<unsigned>(ctas)), dim3(32 * (kDeep ? kMoeDeepWarps : kMoeWideWarps)), smem, st, 1, g);
+    return launch(k, dim3(static_cast<unsigned>(ctas)), dim3(kMoeThreads), smem, st, 1, g);
 }
 
-// The three launches; the deep kernels where an SM has few tiles.
 template <int kNt>
 macaq_status moe_run(const MoeArgs &g, int sms, cudaStream_t st) {
-    auto deep = [&](int64_t K, int64_t rows) {
-        return std::min(g.E, g.R) * (rows / 32) * (K / 128) < kMoeWideTiles * static_cast<int64_t>(sms);
-    };
-    macaq_status s = deep(g.K, 2 * g.I) ? moe_launch<false, kNt, true>(g, sms, st) : moe_launch<false, kNt, false>(g, sms, st);
-    if (s == MACAQ_OK) s = deep(g.I, g.N) ? moe_launch<true, kNt, true>(g, sms, st) : moe_launch<true, kNt, false>(g, sms, st);
+    macaq_status s = moe_launch<false, kNt>(g, sms, st);
+    if (s == MACAQ_OK) s = moe_launch<true, kNt>(g, sms, st);
     if (s != MACAQ_OK) return s;
     const unsigned warps = static_cast<unsigned>(g.T) * (g.N / 128);
     return launch(moe_sum_kernel, dim3((warps + kMoeSumWarps - 1) / kMoeSumWarps), dim3(32 * kMoeSumWarps), 0, st, 1, g);
@@ -1198,6 +1191,18 @@ macaq_status moe_w4a16(const MoeArgs &a, void *workspace, size_t ws_bytes, cudaS
 }
 
 // ------------------------------------------------------------------------ low-rank adapters
+template <int kMt, bool kF32>
+macaq_status run_lora(const LoraArgs &g, cudaStream_t st) {
+    auto k = lora_add_kernel<kMt, kF32>;
+    const size_t smem = lora_smem_bytes(g.r, kMt, kF32 ? 3 : 2);
+    macaq_status s = set_smem(k, smem);
+    if (s != MACAQ_OK) return s;
+    // chunks: one per adapter with rows and one for the rows of none, one more per 16 kMt rows
+    const int64_t chunks = std::min<int64_t>(g.L + 1, g.M) + g.M / (16 * kMt);
+    if (chunks * kLoraCluster >= (int64_t(1) << 31)) return MACAQ_ERR_SHAPE;
+    return launch(k, dim3(static_cast<unsigned>(chunks * kLoraCluster)), dim3(kLoraThreads), smem, st, kLoraCluster, g);
+}
+
 macaq_status lora_add(const LoraArgs &p, int32_t dtype, cudaStream_t st) {
     constexpr int64_t kMax = int64_t(1) << 31;
     if (p.M < 0 || p.M >= kMax || p.K <= 0 || p.K >= kMax || p.N <= 0 || p.N >= kMax || p.K % 8 || p.N % 8 || p.r < 8 ||
@@ -1219,7 +1224,10 @@ macaq_status lora_add(const LoraArgs &p, int32_t dtype, cudaStream_t st) {
     if (s != MACAQ_OK) return s;
     LoraArgs g = p;
     g.f32 = dtype == MACAQ_OUT_F32;
-    return launch(lora_add_kernel, dim3(static_cast<unsigned>(g.M)), dim3(kLoraThreads), 0, st, 1, g);
+    // 64-row chunks once adapters have some: A and B are read per chunk
+    const bool wide = p.M > 32 * static_cast<int64_t>(p.L);
+    if (g.f32) return wide ? run_lora<4, true>(g, st) : run_lora<1, true>(g, st);
+    return wide ? run_lora<4, false>(g, st) : run_lora<1, false>(g, st);
 }
 
 }  // namespace macaq

@@ -16,8 +16,7 @@
 // (128 channels), one per warp, wherever the cuts fall: every warp streams the same number of weights, for one token as
 // for 64. The pieces of a cut item meet in shared memory once the CTA's warps are done. The chunks' operands are
 // fp16 panels in shared memory, made before the CTA streams; each warp streams through its own ring of cp.async stages,
-// without a barrier. "Deep" CTAs, for few items, have 8 warps and half an SM's registers and shared memory, so that
-// kernel 2's fit beside kernel 1's and fill their rings with weights while it runs (programmatic launch); others 16.
+// without a barrier.
 //
 // Arithmetic. m16n8k16 fp16 MMAs with weights as the 16-row operand: a lane's 32-bit word of a row (8 codes of
 // one MX group) becomes four fp16 pairs with one conversion instruction each, exactly, and needs no pass through shared or
@@ -44,12 +43,12 @@
 namespace macaq {
 
 constexpr int kMoeMaxT = 64;
-constexpr int kMoeDeepWarps = 8, kMoeWideWarps = 16;
-constexpr int kMoeDeepStages = 4, kMoeWideStages = 3;
+constexpr int kMoeThreads = 512;
+constexpr int kMoeWarps = kMoeThreads / 32;
+constexpr int kMoeStages = 3;
 constexpr int kMoeStageBytes = 2048 + 128;  // 32 rows x 64 code bytes, 8 scale chunks
-constexpr int kMoeWideTiles = 128;          // K tiles per SM from which the wide kernels are used
 constexpr int kMoeMaxPanels = 8;
-constexpr int kMoeGroupUnroll = 2;         // MX groups of a tile in straight code
+constexpr int kMoeGroupUnroll = 4;         // MX groups of a tile in straight code
 
 struct MoeArgs {
     const uint16_t *x;            // bf16 [T, K]
@@ -78,17 +77,13 @@ __host__ __device__ constexpr int moe_panel_stride(int tiles) { return tiles * 2
 __host__ __device__ constexpr int moe_row_bytes(int tiles) { return moe_panel_stride(tiles) + tiles * 16; }
 // Dynamic shared memory: rings, first pieces of cut items (one per warp), panel rows, their 1 / s, flags [panel][tile] (some s
 // of the tile is not 1), chunk table.
-__host__ __device__ constexpr int moe_heads_offset(bool deep) {
-    return (deep ? kMoeDeepWarps * kMoeDeepStages : kMoeWideWarps * kMoeWideStages) * kMoeStageBytes;
+__host__ __device__ constexpr int moe_heads_offset() { return kMoeWarps * kMoeStages * kMoeStageBytes; }
+__host__ __device__ constexpr int moe_panels_offset(int nt) { return moe_heads_offset() + kMoeWarps * 1024 * nt; }
+__host__ __device__ constexpr int moe_flags_offset(int nt, int tiles, int rows) {
+    return moe_panels_offset(nt) + rows * moe_row_bytes(tiles);
 }
-__host__ __device__ constexpr int moe_panels_offset(int nt, bool deep) {
-    return moe_heads_offset(deep) + (deep ? kMoeDeepWarps : kMoeWideWarps) * 1024 * nt;
-}
-__host__ __device__ constexpr int moe_flags_offset(int nt, bool deep, int tiles, int rows) {
-    return moe_panels_offset(nt, deep) + rows * moe_row_bytes(tiles);
-}
-__host__ __device__ constexpr int moe_table_offset(int nt, bool deep, int tiles, int rows) {
-    return moe_flags_offset(nt, deep, tiles, rows) + kMoeMaxPanels * tiles * 4;
+__host__ __device__ constexpr int moe_table_offset(int nt, int tiles, int rows) {
+    return moe_flags_offset(nt, tiles, rows) + kMoeMaxPanels * tiles * 4;
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
@@ -291,7 +286,7 @@ struct MoeRow {
 };
 
 // after_loads() runs once the first loads are on their way.
-template <bool kDown, int kThreads, typename AfterLoads>
+template <bool kDown, typename AfterLoads>
 __device__ __forceinline__ void moe_fill_panels(const MoeArgs &a, const MoeChunk *chunks, const MoeRow *rows, int count, uint8_t *panel,
                                                 float *xs, int32_t *flags, AfterLoads after_loads) {
     const int width = kDown ? a.I : a.K, units = width / 8, total = count * units, lane = threadIdx.x & 31;
@@ -300,12 +295,12 @@ __device__ __forceinline__ void moe_fill_panels(const MoeArgs &a, const MoeChunk
     constexpr int kAtOnce = 2;   // units whose loads are in flight
     bool first = true;
 #pragma unroll 1
-    for (int base = threadIdx.x & ~31; base < total; base += kAtOnce * kThreads) {
+    for (int base = threadIdx.x & ~31; base < total; base += kAtOnce * kMoeThreads) {
         float4 f[kAtOnce][2], m[kAtOnce][2];
         int row[kAtOnce], c[kAtOnce], chunk[kAtOnce];
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k) {
-            const int u = min(base + k * kThreads + lane, total - 1);
+            const int u = min(base + k * kMoeThreads + lane, total - 1);
             row[k] = u / units;
             c[k] = u - row[k] * units;
             const MoeRow r = rows[row[k]];
@@ -326,7 +321,7 @@ __device__ __forceinline__ void moe_fill_panels(const MoeArgs &a, const MoeChunk
         first = false;
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k) {
-            if (base + k * kThreads >= total) break;
+            if (base + k * kMoeThreads >= total) break;
             float v[8];
             if constexpr (kDown) {
                 v[0] = f[k][0].x, v[1] = f[k][0].y, v[2] = f[k][0].z, v[3] = f[k][0].w;
@@ -344,7 +339,7 @@ __device__ __forceinline__ void moe_fill_panels(const MoeArgs &a, const MoeChunk
             v[4] *= m[k][1].x, v[5] *= m[k][1].y, v[6] *= m[k][1].z, v[7] *= m[k][1].w;
             uint4 h;
             const float inv = moe_to_half(v, kDown ? a.b_dn : a.b_gu, h);
-            if (base + k * kThreads + lane < total) {
+            if (base + k * kMoeThreads + lane < total) {
                 *reinterpret_cast<uint4 *>(panel + row[k] * stride + c[k] * 16) = h;
                 if ((lane & 3) == 0) {
                     xs[row[k] * (width / 32) + c[k] / 4] = inv;
@@ -357,7 +352,6 @@ __device__ __forceinline__ void moe_fill_panels(const MoeArgs &a, const MoeChunk
 }
 
 // The weight stream of one warp: the K tiles of consecutive items. issue() starts the copies of the next tile.
-template <int kStages>
 struct MoeStream {
     const uint8_t *wq, *wsf;
     const MoeChunk *table;
@@ -378,7 +372,7 @@ struct MoeStream {
         z = z_, r = r_, tile = tile_, left = count, slot = 0;
         if (left > 0) point();
 #pragma unroll 1
-        for (int i = 0; i < kStages - 1; ++i) issue();
+        for (int i = 0; i < kMoeStages - 1; ++i) issue();
     }
     __device__ __forceinline__ void issue() {
         const int lane = threadIdx.x & 31;
@@ -399,7 +393,7 @@ struct MoeStream {
                 if (left > 0) point();
             }
         }
-        slot = slot == kStages - 1 ? 0 : slot + 1;
+        slot = slot == kMoeStages - 1 ? 0 : slot + 1;
         cp_async_commit();   // an empty group keeps groups and stages in step
     }
 };
@@ -425,92 +419,70 @@ __device__ __forceinline__ void moe_store_item(const MoeArgs &a, const MoeChunk 
         }
 }
 
-// kDown = false: kernel 1; true: kernel 2. kDeep: one CTA per SM and few tiles per warp, where a launch is mostly
-// latency. A deep kernel goes through its panel and tile code once on whatever is in memory before it waits for the kernel
-// ahead of it, so that the instructions are cached when the operands arrive; what that pass computes is dropped. Measured
-// for one token of 128 experts, top-8, 2048 x 768: the first tile after the wait took 2.2 us without the pass.
-template <bool kDown, int kNt, bool kDeep>
-__global__ void __launch_bounds__(32 * (kDeep ? kMoeDeepWarps : kMoeWideWarps), kDeep ? 2 : 1) moe_w4a16_kernel(MoeArgs a) {
-    constexpr int kStages = kDeep ? kMoeDeepStages : kMoeWideStages, kWarps = kDeep ? kMoeDeepWarps : kMoeWideWarps;
-    constexpr int kThreads = 32 * kWarps;
-    extern __shared__ __align__(128) uint8_t s_raw[];
+// kDown = false: kernel 1; true: kernel 2.
+template <bool kDown, int kNt>
+__global__ void __launch_bounds__(kMoeThreads, 1) moe_w4a16_kernel(MoeArgs a) {
+    extern __shared__ __align__(128) uint8_t s_moe[];
     __shared__ MoeRow s_rows[kMoeMaxPanels * 8 * kNt];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    if constexpr (kDown) griddep_launch_dependents();
+    // Kernel 1 waits for everything before it and only then lets kernel 2 start, so the plan and the weights are complete
+    // for both; kernel 2 waits for kernel 1's rows before it reads them.
+    if constexpr (!kDown) griddep_wait();
+    griddep_launch_dependents();
 
     const int kt = (kDown ? a.I : a.K) / 128, stride = moe_panel_stride(kt);
-    float *heads = reinterpret_cast<float *>(s_raw + moe_heads_offset(kDeep));
-    uint8_t *panel = s_raw + moe_panels_offset(kNt, kDeep);
+    float *heads = reinterpret_cast<float *>(s_moe + moe_heads_offset());
+    uint8_t *panel = s_moe + moe_panels_offset(kNt);
     float *xs = reinterpret_cast<float *>(panel + a.panel_rows * stride);   // [row][group]
-    int32_t *flags = reinterpret_cast<int32_t *>(s_raw + moe_flags_offset(kNt, kDeep, kt, a.panel_rows));
-    MoeChunk *table = reinterpret_cast<MoeChunk *>(s_raw + moe_table_offset(kNt, kDeep, kt, a.panel_rows));
+    int32_t *flags = reinterpret_cast<int32_t *>(s_moe + moe_flags_offset(kNt, kt, a.panel_rows));
+    MoeChunk *table = reinterpret_cast<MoeChunk *>(s_moe + moe_table_offset(kNt, kt, a.panel_rows));
 
-    MoeStream<kStages> w;
+    MoeStream w;
     w.wq = kDown ? a.wq_dn : a.wq_gu;
     w.wsf = kDown ? a.wsf_dn : a.wsf_gu;
     w.table = table;
-    w.ring = smem_u32(s_raw) + warp * kStages * kMoeStageBytes;
+    w.ring = smem_u32(s_moe) + warp * kMoeStages * kMoeStageBytes;
     w.st = g * 64 + ((t ^ ((g >> 1) & 3)) << 4);
     w.K = 128 * kt;
     w.tiles = kt;
     w.per_chunk = (kDown ? a.N : 2 * a.I) / 32;
     const uint32_t ld = (lane >> 3) * 512 + (lane & 7) * 64 + (((lane >> 1) & 3) << 4);   // ldmatrix: row lane % 8 of quarter lane / 8
 
-    int begin = 0, end = 0, from = 0, to = 0;   // items: of the CTA, of the phase
-    int z = 0, r = 0;                           // item `from` is number r of the table's chunk z
-    int chunks = 1, rows = 1, total = 0, first = 0, last = 1, tile = 0, item_z = 0, item_r = 0;
-    bool found = false, prepared = false, dry = kDeep;
-    for (;;) {
-        // Kernel 1 waits for everything before it and only then lets kernel 2 start, so the plan and the weights are
-        // complete for both; kernel 2 waits for kernel 1's rows before it reads them.
-        if (!found && (kDown || !dry)) {
-            if constexpr (!kDown) {
-                griddep_wait();
-                griddep_launch_dependents();
-            }
-            moe_find_items(a, blockIdx.x, gridDim.x, w.per_chunk, reinterpret_cast<int32_t *>(panel), table, begin, end, r);
-            from = begin;
-            found = true;
+    int begin, end, r, z = 0;   // the CTA's items; the next one is number r of the table's chunk z
+    moe_find_items(a, blockIdx.x, gridDim.x, w.per_chunk, reinterpret_cast<int32_t *>(panel), table, begin, end, r);
+    if constexpr (kDown)
+        if (begin >= end) griddep_wait();   // nothing after this grid runs before kernel 1 ends
+    for (int from = begin; from < end;) {
+        // a phase: the items of as many chunks as have their panel rows in shared memory at a time
+        int chunks = 0, rows = 0, to = from;
+        while (to < end && chunks < kMoeMaxPanels && rows + table[z + chunks].rows <= a.panel_rows) {
+            rows += table[z + chunks].rows;
+            to = min(end, to + w.per_chunk - (chunks == 0 ? r : 0));
+            ++chunks;
         }
-        auto cut = [&](int i) { return static_cast<int>(static_cast<int64_t>(total) * i / kWarps); };
-        if (found && !prepared) {
-            if (from >= end) break;
-            // a phase: the items of as many chunks as have their panel rows in shared memory at a time
-            chunks = rows = 0;
-            to = from;
-            while (to < end && chunks < kMoeMaxPanels && rows + table[z + chunks].rows <= a.panel_rows) {
-                rows += table[z + chunks].rows;
-                to = min(end, to + w.per_chunk - (chunks == 0 ? r : 0));
-                ++chunks;
-            }
-            total = (to - from) * kt;
-            first = cut(warp), last = cut(warp + 1);
-            item_r = first / kt;   // where this warp starts
-            tile = first - item_r * kt;
-            item_r += r;
-            for (item_z = z; item_r >= w.per_chunk; item_r -= w.per_chunk) ++item_z;
-            if constexpr (kDown) w.start(item_z, item_r, tile, last - first);
-            for (int i = threadIdx.x; i < chunks * 8 * kNt; i += kThreads) {
-                int at = i % (8 * kNt);
-                const MoeChunk ch = table[z + i / (8 * kNt)];
-                if (at >= ch.rows) continue;
-                const int src = kDown ? ch.row0 + at : min(max(__ldcg(a.row_index + ch.row0 + at), 0), a.T - 1);
-                for (int c = 0; c < i / (8 * kNt); ++c) at += table[z + c].rows;
-                s_rows[at] = {i / (8 * kNt), src};
-            }
-            prepared = true;
+        const int total = (to - from) * kt;
+        auto cut = [&](int i) { return static_cast<int>(static_cast<int64_t>(total) * i / kMoeWarps); };
+        const int first = cut(warp), last = cut(warp + 1);
+        int item_z = z, item_r = first / kt;   // where this warp starts
+        int tile = first - item_r * kt;
+        item_r += r;
+        for (; item_r >= w.per_chunk; item_r -= w.per_chunk) ++item_z;
+        if constexpr (kDown) w.start(item_z, item_r, tile, last - first);
+        for (int i = threadIdx.x; i < chunks * 8 * kNt; i += kMoeThreads) {
+            int at = i % (8 * kNt);
+            const MoeChunk ch = table[z + i / (8 * kNt)];
+            if (at >= ch.rows) continue;
+            const int src = kDown ? ch.row0 + at : min(max(__ldcg(a.row_index + ch.row0 + at), 0), a.T - 1);
+            for (int c = 0; c < i / (8 * kNt); ++c) at += table[z + c].rows;
+            s_rows[at] = {i / (8 * kNt), src};
         }
-        if (!found && threadIdx.x == 0) {   // kernel 1's dry pass: row 0 of X
-            table[0] = {0, 0, 1};
-            s_rows[0] = {0, 0};
-        }
-        for (int i = threadIdx.x; i < chunks * kt; i += kThreads) flags[i] = 0;
+        for (int i = threadIdx.x; i < chunks * kt; i += kMoeThreads) flags[i] = 0;
         if constexpr (kDown)
-            if (!dry && from == begin) griddep_wait();
+            if (from == begin) griddep_wait();
         __syncthreads();
         // kernel 1 has its operands on their way before the weights queue up behind them
-        moe_fill_panels<kDown, kThreads>(a, table + z, s_rows, dry ? 1 : rows, panel, xs, flags, [&] {
-            if (!kDown && !dry) w.start(item_z, item_r, tile, last - first);
+        moe_fill_panels<kDown>(a, table + z, s_rows, rows, panel, xs, flags, [&] {
+            if (!kDown) w.start(item_z, item_r, tile, last - first);
         });
         __syncthreads();
 
@@ -535,13 +507,11 @@ __global__ void __launch_bounds__(32 * (kDeep ? kMoeDeepWarps : kMoeWideWarps), 
         int slot = 0;
 #pragma unroll 1
         for (int j = first; j < last; ++j) {
-            if (!dry) {
-                cp_async_wait<kStages - 2>();
-                __syncwarp();   // every lane's copies of this tile have landed, and every lane is done with the tile before
-                w.issue();
-            }
+            cp_async_wait<kMoeStages - 2>();
+            __syncwarp();   // every lane's copies of this tile have landed, and every lane is done with the tile before
+            w.issue();
             const uint32_t stage = w.ring + slot * kMoeStageBytes;
-            slot = slot == kStages - 1 ? 0 : slot + 1;
+            slot = slot == kMoeStages - 1 ? 0 : slot + 1;
             uint32_t word[4];
             asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(word[0]), "=r"(word[1]), "=r"(word[2]), "=r"(word[3])
@@ -549,7 +519,6 @@ __global__ void __launch_bounds__(32 * (kDeep ? kMoeDeepWarps : kMoeWideWarps), 
                          : "memory");
             if (flag[tile]) moe_tile_mma<kNt, true>(stage + ld, word, bcol, x0, x1, tile, acc);
             else moe_tile_mma<kNt, false>(stage + ld, word, bcol, x0, x1, tile, acc);
-            if (dry) break;
             if (++tile == kt) {
                 if (whole) {
                     moe_store_item<kDown, kNt>(a, table[item_z], item_r, acc, lane);
@@ -568,14 +537,7 @@ __global__ void __launch_bounds__(32 * (kDeep ? kMoeDeepWarps : kMoeWideWarps), 
                 }
             }
         }
-        float *tails = reinterpret_cast<float *>(s_raw + warp * kStages * kMoeStageBytes);
-        if (dry) {
-            // keeps the dry pass's sums: the condition never holds (the panel's stride is not 1)
-            if (stride == 1) heads[lane] = acc[0][0][0] + acc[1][0][1] + acc[0][0][2] + acc[1][0][3];
-            dry = false;
-            __syncthreads();
-            continue;
-        }
+        float *tails = reinterpret_cast<float *>(s_moe + warp * kMoeStages * kMoeStageBytes);
         cp_async_wait<0>();
         __syncwarp();
         // a piece that its item's end does not close: the warp's first if it starts inside the item, else over its ring
@@ -589,10 +551,10 @@ __global__ void __launch_bounds__(32 * (kDeep ? kMoeDeepWarps : kMoeWideWarps), 
         const int whole_items = first / kt;
         if (first != whole_items * kt && warp > 0 && cut(warp - 1) <= whole_items * kt) {
             const int stop = (whole_items + 1) * kt;
-            const float *before = reinterpret_cast<const float *>(s_raw + (warp - 1) * kStages * kMoeStageBytes);
+            const float *before = reinterpret_cast<const float *>(s_moe + (warp - 1) * kMoeStages * kMoeStageBytes);
 #pragma unroll
             for (int i = 0; i < 8 * kNt; ++i) acc[i / (4 * kNt)][i / 4 % kNt][i % 4] = before[i * 32 + lane];
-            for (int v = warp; v < kWarps && cut(v) < stop; ++v) {
+            for (int v = warp; v < kMoeWarps && cut(v) < stop; ++v) {
                 if (cut(v) == cut(v + 1)) continue;
 #pragma unroll
                 for (int i = 0; i < 8 * kNt; ++i) acc[i / (4 * kNt)][i / 4 % kNt][i % 4] += heads[(v * 8 * kNt + i) * 32 + lane];
@@ -608,11 +570,8 @@ __global__ void __launch_bounds__(32 * (kDeep ? kMoeDeepWarps : kMoeWideWarps), 
             ++z;
         }
         from = to;
-        prepared = false;
-        __syncthreads();   // panels and pieces are read before the next phase writes them
+        if (from < end) __syncthreads();   // panels and pieces are read before the next phase writes them
     }
-    if constexpr (kDown)
-        if (begin >= end) griddep_wait();   // nothing after this grid runs before kernel 1 ends
 }
 
 // The weighted sum of each token's choices, in the order j = 0, 1, ...: a warp takes 128 outputs of a token.
