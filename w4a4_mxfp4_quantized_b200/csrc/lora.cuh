@@ -43,10 +43,12 @@ struct LoraArgs {
     int32_t r, L, f32;
 };
 
-// Shared memory for rank r (rounded up to 32 in the parts of V), chunks of 16 mt rows and `parts` bf16 parts of V: the CTA's
-// partial V per k split, its sum, the parts of V.
-__host__ __device__ constexpr int lora_rank32(int r) { return (r + 31) / 32 * 32; }
-__host__ __device__ constexpr int lora_v_stride(int r) { return lora_rank32(r) + 8; }   // bf16: rows 16 bytes off a multiple of 64
+// Shared memory for rank r, chunks of 16 mt rows and `parts` bf16 parts of V: the CTA's partial V per k split, its sum, the
+// parts of V. The parts' rows have the rank of the kernel that serves r (32 kSteps), zero from r on.
+__host__ __device__ constexpr int lora_padded_rank(int r) { return r <= 32 ? 32 : (r <= 64 ? 64 : 128); }
+__host__ __device__ constexpr int lora_v_stride(int r) {   // bf16; 64 bytes off a multiple of 128: no bank conflicts
+    return lora_padded_rank(r) == 32 ? 32 : lora_padded_rank(r) + 32;
+}
 __host__ __device__ constexpr int lora_splits(int mt) { return kLoraWarps / mt; }
 __host__ __device__ constexpr int lora_smem_bytes(int r, int mt, int parts) {
     return (lora_splits(mt) + 1) * 16 * mt * r * 4 + parts * 16 * mt * lora_v_stride(r) * 2;
@@ -109,14 +111,10 @@ __device__ __forceinline__ LoraChunk lora_find_chunk(const LoraArgs &p, int z, i
 template <bool kF32>
 struct LoraPiece {
     uint4 v[kF32 ? 2 : 1];
-    __device__ __forceinline__ void load(const void *y, int64_t at, bool on) {
+    __device__ __forceinline__ void load(const char *y, bool on) {
         if (!on) return;
-        if constexpr (kF32) {
-            const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(y) + at);
-            v[0] = __ldcg(p), v[1] = __ldcg(p + 1);
-        } else {
-            v[0] = __ldcg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(y) + at));
-        }
+#pragma unroll
+        for (int i = 0; i < (kF32 ? 2 : 1); ++i) v[i] = __ldcg(reinterpret_cast<const uint4 *>(y) + i);
     }
     __device__ __forceinline__ void add(const float (&d)[8]) {
         if constexpr (kF32) {
@@ -133,24 +131,21 @@ struct LoraPiece {
             }
         }
     }
-    __device__ __forceinline__ void store(void *out, int64_t at, bool on) const {
+    __device__ __forceinline__ void store(char *out, bool on) const {
         if (!on) return;
-        if constexpr (kF32) {
-            uint4 *p = reinterpret_cast<uint4 *>(static_cast<float *>(out) + at);
-            p[0] = v[0], p[1] = v[1];
-        } else {
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + at) = v[0];
-        }
+#pragma unroll
+        for (int i = 0; i < (kF32 ? 2 : 1); ++i) reinterpret_cast<uint4 *>(out)[i] = v[i];
     }
 };
 
-// Grid: one cluster per chunk. kMt: m16 tiles of a chunk.
-template <int kMt, bool kF32>
+// Grid: one cluster per chunk. kMt: m16 tiles of a chunk; kSteps: 32-wide steps of the rank.
+template <int kMt, int kSteps, bool kF32>
 __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
-    constexpr int kRows = 16 * kMt, kSplits = lora_splits(kMt), kParts = kF32 ? 3 : 2;
+    constexpr int kRows = 16 * kMt, kSplits = lora_splits(kMt), kParts = kF32 ? 3 : 2, kElement = kF32 ? 4 : 2;
     extern __shared__ __align__(16) uint8_t s_lora[];
     __shared__ int32_t s_off[kRouteMaxExperts + 2];
-    __shared__ int64_t s_row[kRows];   // row of X, Y and out, -1: none
+    __shared__ int64_t s_row[kRows];                // row of X, Y and out, -1: none
+    __shared__ int64_t s_y[kRows], s_out[kRows];    // their offsets in Y and out in bytes
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -165,6 +160,8 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
         int64_t m = -1;
         if (i < ch.rows) m = p.row_index ? static_cast<int64_t>(__ldcg(p.row_index + ch.row0 + i)) : ch.row0 + i;
         s_row[i] = m >= 0 && m < p.M ? m : -1;
+        s_y[i] = m * p.ldy * kElement;
+        s_out[i] = m * p.ldo * kElement;
     }
     __syncthreads();
 
@@ -173,8 +170,8 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
         for (int64_t i = threadIdx.x; i < ch.rows * per; i += kLoraThreads) {
             const int64_t m = s_row[i / per], n = n_begin * 32 + i % per * 8;
             LoraPiece<kF32> y;
-            y.load(p.y, m * p.ldy + n, m >= 0 && n < p.N);
-            y.store(p.out, m * p.ldo + n, m >= 0 && n < p.N);
+            y.load(static_cast<const char *>(p.y) + (m * p.ldy + n) * kElement, m >= 0 && n < p.N);
+            y.store(static_cast<char *>(p.out) + (m * p.ldo + n) * kElement, m >= 0 && n < p.N);
         }
         return;
     }
@@ -195,7 +192,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
         const int mt = warp % kMt, split = warp / kMt;
         const int64_t row_lo = s_row[16 * mt + g], row_hi = s_row[16 * mt + g + 8];
         const uint16_t *x_lo = p.x + row_lo * p.ldx + 8 * t, *x_hi = p.x + row_hi * p.ldx + 8 * t;
-        constexpr int kTiles = 4;   // n8 tiles of V at a time
+        constexpr int kTiles = kSteps == 1 ? 4 : 8;   // n8 tiles of V at a time
         for (int j0 = 0; j0 < r; j0 += 8 * kTiles) {
             float acc[kTiles][4] = {};
 #pragma unroll 2
@@ -222,9 +219,9 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
                 }
         }
     }
-    // the parts' columns from r to the next multiple of 32 are zero
-    for (int i = threadIdx.x; i < kParts * kRows * (lora_rank32(r) - r); i += kLoraThreads) {
-        const int per = lora_rank32(r) - r;
+    // the parts' columns past r are zero
+    for (int i = threadIdx.x; i < kParts * kRows * (lora_padded_rank(r) - r); i += kLoraThreads) {
+        const int per = lora_padded_rank(r) - r;
         v_s[i / per * vs + r + i % per] = 0;
     }
     __syncthreads();
@@ -234,6 +231,36 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
         for (int s = 0; s < kSplits; ++s) v += part[s * kRows * r + i];
         mine[i] = v;
     }
+    // The second product's loads. A warp takes every eighth 32-column step, kBatch of them at a time; the first batch sets out
+    // here, before V is complete. Logical column c of n8 tile i is column 8 (c / 2) + 2 i + c % 2 of the step.
+    constexpr int kBatch = kMt > 1 || kSteps == 4 ? 1 : (kSteps == 1 && !kF32 ? 4 : 2);
+    const int N = static_cast<int>(p.N), s_end = static_cast<int>(n_end), n_lane = 8 * (g >> 1) + (g & 1);
+    int s = static_cast<int>(n_begin) + warp;
+    uint4 b[kBatch][kSteps][4];
+    LoraPiece<kF32> y[kMt > 1 ? 2 : kBatch][2];
+    const uint16_t *b_lane = B + static_cast<int64_t>(n_lane) * r + 8 * t;
+    auto load_y = [&](int step, int mt, LoraPiece<kF32> (&to)[2]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int row = 16 * mt + 8 * h + g;
+            to[h].load(static_cast<const char *>(p.y) + s_y[row] + (step * 32 + 8 * t) * kElement,
+                       s_row[row] >= 0 && step * 32 + 8 * t < N);
+        }
+    };
+    auto load_batch = [&] {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int step = s + u * kLoraWarps;
+            if (step < s_end) load_y(step, 0, y[kMt > 1 ? 0 : u]);
+#pragma unroll
+            for (int ks = 0; ks < kSteps; ++ks)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    b[u][ks][i] = lora_ld(b_lane + (static_cast<int64_t>(step) * 32 + 2 * i) * r + 32 * ks,
+                                          step < s_end && step * 32 + n_lane + 2 * i < N && 32 * ks + 8 * t < r);
+        }
+    };
+    load_batch();
     cluster_sync();
     {   // entries in pairs, an eighth of them per CTA: sum over the cluster, times scale, to everybody in bf16 parts
         const float scale = p.scale ? __ldg(p.scale + ch.a) : 1.0f;
@@ -268,59 +295,48 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
     __syncwarp();
     cluster_sync();
 
-    // out = Y + V B^T: a warp takes every eighth 32-column step for all rows. Logical column c of n8 tile i is column
-    // 8 (c / 2) + 2 i + c % 2 of the step.
-    const int steps = lora_rank32(r) / 32;
-    constexpr int kPair = kMt < 2 ? 1 : 2;   // m16 tiles at a time: their sums and pieces of Y fit in registers
-    for (int64_t s = n_begin + warp; s < n_end; s += kLoraWarps) {
-        const int64_t n0 = s * 32;
-        const bool on = n0 + 8 * t < p.N;
+    // out = Y + V B^T, all rows of 32 columns at a time, tile by tile of 16 rows
 #pragma unroll 1
-        for (int m0 = 0; m0 < kMt; m0 += kPair) {
-            if (16 * m0 >= ch.rows) break;
-            LoraPiece<kF32> y[kPair][2];
+    for (;;) {
 #pragma unroll
-            for (int mt = 0; mt < kPair; ++mt)
+        for (int u = 0; u < kBatch; ++u) {
+            const int step = s + u * kLoraWarps;
+            if (step >= s_end) break;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int64_t m = s_row[16 * (m0 + mt) + 8 * h + g];
-                    y[mt][h].load(p.y, m * p.ldy + n0 + 8 * t, on && m >= 0);
+            for (int mt = 0; mt < kMt; ++mt) {
+                if (16 * mt >= ch.rows) break;
+                if constexpr (kMt > 1) {   // the next tile's Y on its way
+                    if (mt + 1 < kMt) load_y(step, mt + 1, y[(mt + 1) & 1]);
                 }
-            float acc[kPair][4][4] = {};
-#pragma unroll 1
-            for (int ks = 0; ks < steps; ++ks) {
-                const int k = ks * 32 + 8 * t;
-                uint4 b[4];
+                LoraPiece<kF32>(&yt)[2] = y[kMt > 1 ? (mt & 1) : u];
+                float acc[4][4] = {};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int64_t n = n0 + 8 * (g >> 1) + 2 * i + (g & 1);
-                    b[i] = lora_ld(B + n * r + k, n < p.N && k < r);
-                }
-#pragma unroll
-                for (int mt = 0; mt < kPair; ++mt)
+                for (int ks = 0; ks < kSteps; ++ks)
 #pragma unroll
                     for (int q = 0; q < kParts; ++q) {
-                        const uint16_t *v = v_s + (q * kRows + 16 * (m0 + mt) + g) * vs + k;
+                        const uint16_t *v = v_s + (q * kRows + 16 * mt + g) * vs + 32 * ks + 8 * t;
                         const uint4 lo = *reinterpret_cast<const uint4 *>(v), hi = *reinterpret_cast<const uint4 *>(v + 8 * vs);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            mma_bf16(acc[mt][i], lo.x, hi.x, lo.y, hi.y, b[i].x, b[i].y);
-                            mma_bf16(acc[mt][i], lo.z, hi.z, lo.w, hi.w, b[i].z, b[i].w);
+                            mma_bf16(acc[i], lo.x, hi.x, lo.y, hi.y, b[u][ks][i].x, b[u][ks][i].y);
+                            mma_bf16(acc[i], lo.z, hi.z, lo.w, hi.w, b[u][ks][i].z, b[u][ks][i].w);
                         }
                     }
-            }
-#pragma unroll
-            for (int mt = 0; mt < kPair; ++mt)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float d[8];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) d[2 * i] = acc[mt][i][2 * h], d[2 * i + 1] = acc[mt][i][2 * h + 1];
-                    const int64_t m = s_row[16 * (m0 + mt) + 8 * h + g];
-                    y[mt][h].add(d);
-                    y[mt][h].store(p.out, m * p.ldo + n0 + 8 * t, on && m >= 0);
+                    for (int i = 0; i < 4; ++i) d[2 * i] = acc[i][2 * h], d[2 * i + 1] = acc[i][2 * h + 1];
+                    const int row = 16 * mt + 8 * h + g;
+                    yt[h].add(d);
+                    yt[h].store(static_cast<char *>(p.out) + s_out[row] + (step * 32 + 8 * t) * kElement,
+                                s_row[row] >= 0 && step * 32 + 8 * t < N);
                 }
+            }
         }
+        s += kBatch * kLoraWarps;
+        if (s >= s_end) break;
+        load_batch();
     }
 }
 

@@ -1191,9 +1191,9 @@ macaq_status moe_w4a16(const MoeArgs &a, void *workspace, size_t ws_bytes, cudaS
 }
 
 // ------------------------------------------------------------------------ low-rank adapters
-template <int kMt, bool kF32>
-macaq_status run_lora(const LoraArgs &g, cudaStream_t st) {
-    auto k = lora_add_kernel<kMt, kF32>;
+template <int kMt, int kSteps, bool kF32>
+macaq_status run_lora_steps(const LoraArgs &g, cudaStream_t st) {
+    auto k = lora_add_kernel<kMt, kSteps, kF32>;
     const size_t smem = lora_smem_bytes(g.r, kMt, kF32 ? 3 : 2);
     macaq_status s = set_smem(k, smem);
     if (s != MACAQ_OK) return s;
@@ -1201,6 +1201,13 @@ macaq_status run_lora(const LoraArgs &g, cudaStream_t st) {
     const int64_t chunks = std::min<int64_t>(g.L + 1, g.M) + g.M / (16 * kMt);
     if (chunks * kLoraCluster >= (int64_t(1) << 31)) return MACAQ_ERR_SHAPE;
     return launch(k, dim3(static_cast<unsigned>(chunks * kLoraCluster)), dim3(kLoraThreads), smem, st, kLoraCluster, g);
+}
+
+template <int kMt, bool kF32>
+macaq_status run_lora(const LoraArgs &g, cudaStream_t st) {
+    if (g.r <= 32) return run_lora_steps<kMt, 1, kF32>(g, st);
+    if (g.r <= 64) return run_lora_steps<kMt, 2, kF32>(g, st);
+    return run_lora_steps<kMt, 4, kF32>(g, st);
 }
 
 macaq_status lora_add(const LoraArgs &p, int32_t dtype, cudaStream_t st) {
