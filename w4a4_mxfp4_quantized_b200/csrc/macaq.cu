@@ -1040,11 +1040,20 @@ bool plan_shape_ok(int64_t T, int32_t topk, int32_t E) {
     return T >= 0 && topk >= 1 && E >= 1 && E <= kRouteMaxExperts && T <= ((int64_t(1) << 30) - 1) / topk;
 }
 
-macaq_status run_row_groups(const GroupArgs &g, cudaStream_t st) {
-    const size_t smem = (kGroupThreads / 32 + 1) * static_cast<size_t>(g.E + 1) * sizeof(int32_t);
-    macaq_status s = set_smem(row_groups_kernel, smem);
+// The row sort; kVpl > 0: with the choice of experts before it.
+template <int kVpl>
+macaq_status run_row_groups(const RouteArgs &t, const GroupArgs &g, cudaStream_t st) {
+    const size_t smem = (kGroupWarps + 2) * static_cast<size_t>(g.E + 1) * sizeof(int32_t);
+    macaq_status s = set_smem(row_groups_kernel<kVpl>, smem);
     if (s != MACAQ_OK) return s;
-    return launch(row_groups_kernel, dim3(1), dim3(kGroupThreads), smem, st, 1, g);
+    const bool wide = g.R > kGroupWide;   // 16 CTAs: beyond the portable cluster size, hence allowed explicitly
+    if (wide) {
+        const cudaError_t e = cudaFuncSetAttribute(row_groups_kernel<kVpl>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return cuda_fail(e);
+    }
+    const int ctas = wide ? 2 * kGroupCluster
+                          : (g.R > kGroupOneCta || (kVpl > 0 && g.R / g.topk > kGroupWarps) ? kGroupCluster : 1);
+    return launch(row_groups_kernel<kVpl>, dim3(ctas), dim3(kGroupThreads), smem, st, ctas, t, g, ctas);
 }
 
 macaq_status row_groups(const int32_t *ids, int64_t T, int32_t topk, int32_t E, int32_t *offsets, int32_t *row_index,
@@ -1063,7 +1072,7 @@ macaq_status row_groups(const int32_t *ids, int64_t T, int32_t topk, int32_t E, 
     g.offsets = offsets;
     g.row_index = row_index;
     g.pos = pos;
-    return run_row_groups(g, st);
+    return run_row_groups<0>(RouteArgs{}, g, st);
 }
 
 template <int kVpl>
@@ -1101,6 +1110,14 @@ macaq_status moe_route(const void *logits, int32_t in_dtype, int64_t ld, int64_t
         a.scale = scale;
         a.weights = weights;
         a.ids = ids;
+        if (T <= kRouteFusedTokens && E <= 512) {   // more experts per lane would not fit a 1,024-thread CTA's registers
+            const GroupArgs g{ids, T * topk, topk, E, offsets, row_index, pos};
+            if (E <= 32) return run_row_groups<1>(a, g, st);
+            if (E <= 64) return run_row_groups<2>(a, g, st);
+            if (E <= 128) return run_row_groups<4>(a, g, st);
+            if (E <= 256) return run_row_groups<8>(a, g, st);
+            return run_row_groups<16>(a, g, st);
+        }
         const int64_t want = (T + kRouteWarps - 1) / kRouteWarps;
         const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(want, static_cast<int64_t>(dev.sms) * 8));
         if (E <= 32) s = run_route_topk<1>(a, blocks, st);

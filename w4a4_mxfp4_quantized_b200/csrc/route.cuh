@@ -12,6 +12,10 @@
 // Row plan: a stable counting sort of the R = T * topk choices by group. group_offsets[g] is the first sorted
 // row of group g, pos[i] the sorted row of entry i (-1 for an id outside [0, E)), row_index[r] the token
 // (entry / topk) of sorted row r; entries of no group follow the last group in their order.
+//
+// Bound by latency: a prefill's 65,536 entries are 0.8 MB. One CTA sorts up to 2,048 entries, a cluster of eight CTAs more
+// (their counts meet in distributed shared memory, so one launch and no workspace do); with up to 512 tokens the
+// same launch chooses the experts too, a warp per token.
 #pragma once
 
 #include <stdint.h>
@@ -23,7 +27,12 @@ namespace macaq {
 constexpr int kRouteMaxExperts = 1024;
 constexpr int kRouteMaxTopk = 32;
 constexpr int kRouteWarps = 8;          // tokens in flight per CTA of the top-k kernel
-constexpr int kGroupThreads = 1024;     // the row plan: one CTA
+constexpr int kGroupThreads = 1024;
+constexpr int kGroupWarps = kGroupThreads / 32;
+constexpr int kGroupCluster = 8;
+constexpr int kGroupOneCta = 2048;       // entries that one CTA sorts
+constexpr int kGroupWide = 16384;        // entries from which the cluster has 16 CTAs
+constexpr int kRouteFusedTokens = 256;   // tokens whose experts are chosen in the same launch: one per warp of a cluster
 
 struct RouteArgs {
     const void *logits;     // [T, E] bf16 or fp32, rows `ld` elements apart
@@ -130,56 +139,86 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_topk_kernel(RouteArgs 
         route_token<kVpl>(a, t, lane);
 }
 
-// The row plan by one CTA. Warp w owns a contiguous piece of the entries; it walks it 32 at a time, and the lanes
-// with the same group find one another (match_any), so ranks follow the entries' order and nothing is
-// atomic. Shared memory: counts [warps][E + 1] (bucket E: no group), then the buckets' first rows [E + 1].
-__global__ void __launch_bounds__(kGroupThreads) row_groups_kernel(GroupArgs a) {
+// The lanes of `live` whose bucket equals this lane's, by one vote per bit (measured against match.any: see row_groups).
+__device__ __forceinline__ uint32_t group_peers(uint32_t live, int b, int bits) {
+    uint32_t peers = live;
+    for (int i = 0; i < bits; ++i) {
+        const uint32_t set = __ballot_sync(live, (b >> i) & 1);
+        peers &= ((b >> i) & 1) ? set : ~set;
+    }
+    return peers;
+}
+
+// The row plan, by one CTA or a cluster (`ctas`): CTA c owns a contiguous piece of the tokens, each of its warps a
+// contiguous piece of their entries. A warp walks its piece 32 entries at a time, and the lanes with the same group find
+// one another (match_any), so ranks follow the entries' order and nothing is atomic; an entry's rank among the
+// warp's entries of its group waits in pos. Shared memory: counts [warps][E + 1] (bucket E: no group), the CTA's totals
+// [E + 1], the buckets' first rows [E + 1]. kVpl > 0: choose the experts first (kVpl per lane).
+template <int kVpl>
+__global__ void __launch_bounds__(kGroupThreads) row_groups_kernel(RouteArgs t, GroupArgs a, int ctas) {
     extern __shared__ int32_t s_counts[];
-    __shared__ int32_t s_warp[32];
+    __shared__ int32_t s_warp[kGroupWarps];
     griddep_wait();
     griddep_launch_dependents();
-    constexpr int kWarps = kGroupThreads / 32;
     const int B = a.E + 1;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int32_t *mine = s_counts + warp * B;
-    for (int i = threadIdx.x; i < kWarps * B; i += kGroupThreads) s_counts[i] = 0;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
+    int32_t *mine = s_counts + warp * B, *totals = s_counts + kGroupWarps * B, *first = totals + B;
+    const int64_t T = a.R / a.topk, t_begin = T * cta / ctas, t_end = T * (cta + 1) / ctas;
+    for (int i = threadIdx.x; i < kGroupWarps * B; i += kGroupThreads) s_counts[i] = 0;
+    if constexpr (kVpl > 0)
+        for (int64_t tok = t_begin + warp; tok < t_end; tok += kGroupWarps) route_token<kVpl>(t, tok, lane);
     __syncthreads();
-    const int64_t piece = ((a.R + kWarps - 1) / kWarps + 31) / 32 * 32;
-    const int64_t begin = warp * piece, end = min(a.R, begin + piece);
-    auto bucket = [&](int64_t i) {
-        const int32_t id = a.ids[i];
-        return (id >= 0 && id < a.E) ? id : a.E;
-    };
-    for (int64_t i0 = begin; i0 < end; i0 += 32) {
-        const int64_t i = i0 + lane;
-        const bool on = i < end;
-        const uint32_t live = __ballot_sync(0xffffffffu, on);
-        if (on) {
-            const int b = bucket(i);
-            const uint32_t peers = __match_any_sync(live, b);
-            if (lane == __ffs(peers) - 1) mine[b] += __popc(peers);
+    const int64_t e_begin = t_begin * a.topk, e_end = t_end * a.topk;
+    const int64_t piece = ((e_end - e_begin + kGroupWarps - 1) / kGroupWarps + 31) / 32 * 32;
+    const int64_t begin = e_begin + warp * piece, end = min(e_end, begin + piece);
+    auto bucket = [&](int32_t id) { return id >= 0 && id < a.E ? id : a.E; };
+    const int bits = 32 - __clz(a.E);   // of a bucket number
+    constexpr int kAhead = 4;           // ids in flight
+    for (int64_t i0 = begin; i0 < end; i0 += 32 * kAhead) {
+        int32_t id[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) id[k] = i0 + 32 * k + lane < end ? __ldcg(a.ids + i0 + 32 * k + lane) : 0;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int64_t i = i0 + 32 * k + lane;
+            const bool on = i < end;
+            const uint32_t live = __ballot_sync(0xffffffffu, on);
+            if (on) {
+                const int b = bucket(id[k]);
+                const uint32_t peers = group_peers(live, b, bits);
+                const int32_t before = mine[b];
+                a.pos[i] = before + __popc(peers & ((1u << lane) - 1));
+                __syncwarp(live);
+                if (lane == __ffs(peers) - 1) mine[b] = before + __popc(peers);
+            }
+            __syncwarp();
         }
-        __syncwarp();
     }
     __syncthreads();
-    // per bucket: exclusive prefix over the warps; then an exclusive scan of the buckets' totals (one per thread,
-    // E + 1 <= 1025 buckets: the last one starts where the groups end)
-    int32_t total = 0;
-    const int b = threadIdx.x;
-    if (b < a.E)
-        for (int w = 0; w < kWarps; ++w) {
+    // per bucket: exclusive prefix over the CTA's warps, and the CTA's total
+    for (int b = threadIdx.x; b < B; b += kGroupThreads) {
+        int32_t sum = 0;
+#pragma unroll 8
+        for (int w = 0; w < kGroupWarps; ++w) {
             const int32_t c = s_counts[w * B + b];
-            s_counts[w * B + b] = total;
-            total += c;
+            s_counts[w * B + b] = sum;
+            sum += c;
         }
-    if (threadIdx.x == 0) {
-        int32_t rest = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            const int32_t c = s_counts[w * B + a.E];
-            s_counts[w * B + a.E] = rest;
-            rest += c;
-        }
+        totals[b] = sum;
     }
+    if (ctas > 1) cluster_sync();
+    else __syncthreads();
+    // the bucket's rows in the CTAs before this one and in all of them
+    const int b = threadIdx.x;
+    int32_t below = 0, total = 0;
+    if (b < a.E)
+        for (int c = 0; c < ctas; ++c) {
+            int32_t v = totals[b];
+            if (ctas > 1)
+                asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(map_to_rank(smem_u32(totals + b), c)) : "memory");
+            below += c < cta ? v : 0;
+            total += v;
+        }
     int32_t x = total;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -198,34 +237,44 @@ __global__ void __launch_bounds__(kGroupThreads) row_groups_kernel(GroupArgs a) 
         s_warp[lane] = y;
     }
     __syncthreads();
-    int32_t *first = s_counts + kWarps * B;
-    const int32_t base = x - total + (warp > 0 ? s_warp[warp - 1] : 0);
+    const int32_t base = x - total + (warp > 0 ? s_warp[warp - 1] : 0), live_rows = s_warp[kGroupWarps - 1];
     if (b < a.E) {
-        first[b] = base;
-        a.offsets[b] = base;
+        first[b] = base + below;
+        if (cta == 0) a.offsets[b] = base;
     }
-    if (threadIdx.x == 0) {
-        first[a.E] = s_warp[31];
-        a.offsets[a.E] = s_warp[31];
+    if (threadIdx.x == 0) {   // entries of no group: after the last group
+        int32_t rest = 0;
+        for (int c = 0; c < cta; ++c) {
+            int32_t v;
+            asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(map_to_rank(smem_u32(totals + a.E), c)) : "memory");
+            rest += v;
+        }
+        first[a.E] = live_rows + rest;
+        if (cta == 0) a.offsets[a.E] = live_rows;
     }
     __syncthreads();
-    for (int64_t i0 = begin; i0 < end; i0 += 32) {
-        const int64_t i = i0 + lane;
-        const bool on = i < end;
-        const uint32_t live = __ballot_sync(0xffffffffu, on);
-        int bk = 0;
-        uint32_t peers = 0;
-        if (on) {
-            bk = bucket(i);
-            peers = __match_any_sync(live, bk);
-            const int32_t r = first[bk] + mine[bk] + __popc(peers & ((1u << lane) - 1));
-            a.pos[i] = bk < a.E ? r : -1;
-            a.row_index[r] = static_cast<int32_t>(i / a.topk);
+    for (int64_t i0 = begin; i0 < end; i0 += 32 * kAhead) {
+        int32_t id[kAhead], rank[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int64_t i = i0 + 32 * k + lane;
+            if (i < end) {
+                id[k] = __ldcg(a.ids + i);
+                rank[k] = a.pos[i];   // this thread's own
+            }
         }
-        __syncwarp();
-        if (on && lane == __ffs(peers) - 1) mine[bk] += __popc(peers);
-        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int64_t i = i0 + 32 * k + lane;
+            if (i < end) {
+                const int bk = bucket(id[k]);
+                const int32_t r = first[bk] + mine[bk] + rank[k];
+                a.pos[i] = bk < a.E ? r : -1;
+                a.row_index[r] = static_cast<int32_t>(static_cast<uint32_t>(i) / static_cast<uint32_t>(a.topk));
+            }
+        }
     }
+    if (ctas > 1) cluster_sync();   // no CTA leaves while another reads its totals
 }
 
 }  // namespace macaq
