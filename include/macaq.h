@@ -322,13 +322,16 @@ macaq_status macaq_moe_w4a16(const void *X, int64_t T, int64_t K, const float *w
  *                  (macaq_row_groups with topk = 1). row_index lists every row once: a row listed twice
  *                  gets one of the two results. NULL row_index: the rows are sorted already. Read on the
  *                  device; out-of-range values are clamped or skipped.
+ *   workspace      at least macaq_lora_workspace_bytes(M, r, L, dtype) bytes (0 for few rows: may be NULL then);
+ *                  no initial value needed, nothing kept between calls. Calls that may overlap need separate ones.
  *   K, N, r, ldx, ldy, ldo multiples of 8 (ldy, ldo of fp32: 4); 8 <= r <= 128; 1 <= L <= 1024; M >= 0
  *   (0: no-op); M, K, N < 2^31. Every pointer 16-byte aligned, scale 4-byte.
  */
+size_t macaq_lora_workspace_bytes(int64_t M, int32_t r, int32_t L, int32_t dtype);
 macaq_status macaq_lora_add(const void *Y, int64_t ldy, void *out, int64_t ldo, int32_t dtype, const void *X, int64_t ldx,
                             int64_t M, int64_t K, int64_t N, const void *A, const void *B, int32_t r, int32_t L,
-                            const float *scale, const int32_t *group_offsets, const int32_t *row_index,
-                            macaq_stream_t stream);
+                            const float *scale, const int32_t *group_offsets, const int32_t *row_index, void *workspace,
+                            size_t ws_bytes, macaq_stream_t stream);
 
 /*
  * Dense W4A4 linear: Y[m, n] = sum_k dq(A[m, k]) * dq(W'[n, k]), fp32 accumulation on the tcgen05

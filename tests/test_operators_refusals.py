@@ -58,7 +58,7 @@ def test_moe_w4a16(lib):
 
 def test_lora_add(lib):
     f = caller(lib.macaq_lora_add, Y=P, ldy=256, out=P + 4096, ldo=256, dt=0, X=P, ldx=128, M=4, K=128, N=256, A=P, B=P, r=16, L=3,
-               scale=None, off=P, row=P, st=None)
+               scale=None, off=P, row=P, ws=None, wsb=0, st=None)
     assert f(K=100) == 2 and f(N=100) == 2 and f(r=12) == 2 and f(r=0) == 2 and f(r=136) == 2 and f(L=0) == 2 and f(L=1025) == 2
     assert f(M=-1) == 2 and f(ldx=120) == 2 and f(ldx=132) == 2 and f(ldy=248) == 2 and f(ldy=260) == 2 and f(ldo=252) == 2
     assert f(out=P, ldo=512) == 2                       # in place with another stride
@@ -67,8 +67,11 @@ def test_lora_add(lib):
         assert f(**{name: None}) == 1, name
     for name in ("Y", "out", "X", "A", "B", "off", "row"):
         assert f(**{name: P + 8}) == 3, name
-    assert f(scale=P + 2) == 3
+    assert f(scale=P + 2) == 3 and f(ws=P + 8) == 3
     assert f(M=0) == 0
+    need = mq.lora_workspace_bytes(5000, 16, 3)      # many rows take a workspace
+    assert need > 0 and f(M=5000) == 7 and f(M=5000, ws=P, wsb=need - 1) == 7
+    assert mq.lora_workspace_bytes(5, 12, 3) == 0
 
 
 def test_binding_refuses_cpu_tensors():

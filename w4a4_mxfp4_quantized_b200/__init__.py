@@ -29,6 +29,7 @@ __all__ = [
     "set_wait_limit_ns", "check_group_offsets", "act_quant_gather", "moe_combine",
     "linear_swiglu", "swiglu_act_quant", "interleave_gate_up", "flip_refine", "act_transform", "linear_w4a16",
     "SCORE_SOFTMAX", "SCORE_SIGMOID", "moe_route", "row_groups", "moe_w4a16", "moe_w4a16_workspace_bytes", "lora_add",
+    "lora_workspace_bytes",
     "library_path", "lib",
 ]
 
@@ -80,8 +81,9 @@ _SIGNATURES = {
     "macaq_moe_w4a16_workspace_bytes": ([_i64, _i32, _i32, _i64, _i64, _i64], _sz),
     "macaq_moe_w4a16": ([_vp, _i64, _i64, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _vp, _vp, _vp, _i32,
                          _i64, _vp, _vp, _sz, _vp], ctypes.c_int),
-    "macaq_lora_add": ([_vp, _i64, _vp, _i64, _i32, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp],
-                       ctypes.c_int),
+    "macaq_lora_workspace_bytes": ([_i64, _i32, _i32, _i32], _sz),
+    "macaq_lora_add": ([_vp, _i64, _vp, _i64, _i32, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp,
+                        _sz, _vp], ctypes.c_int),
 }
 
 
@@ -434,6 +436,11 @@ def moe_w4a16(X: torch.Tensor, weights: torch.Tensor, group_offsets: torch.Tenso
     return out
 
 
+@functools.lru_cache(maxsize=1024)
+def lora_workspace_bytes(M: int, r: int, L: int, dtype: int = OUT_BF16) -> int:
+    return int(lib().macaq_lora_workspace_bytes(M, r, L, dtype))
+
+
 def _rows(name: str, t: torch.Tensor, dtype, M: int, N: int, dev):
     """Pointer and row stride of a [M, N] tensor whose rows are contiguous."""
     if t.dtype is not dtype or t.shape != (M, N) or t.get_device() != dev or (N > 1 and t.stride(1) != 1):
@@ -443,7 +450,7 @@ def _rows(name: str, t: torch.Tensor, dtype, M: int, N: int, dev):
 
 
 def lora_add(Y: torch.Tensor, X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, group_offsets: torch.Tensor,
-             row_index: torch.Tensor | None = None, *, scale: torch.Tensor | None = None, out=None):
+             row_index: torch.Tensor | None = None, *, scale: torch.Tensor | None = None, out=None, workspace=None):
     """Low-rank adapters of many requests beside a shared projection: out[m] = Y[m] + scale[a] (X[m] A[a]^T) B[a]^T for the
     rows m of adapter a. Y bf16 or fp32 [M, N] (a column slice is fine), the output of any of the linear calls on X
     bf16 [M, K]; A bf16 [L, r, K], B bf16 [L, N, r], scale fp32 [L] or None. The rows of every adapter:
@@ -459,11 +466,16 @@ def lora_add(Y: torch.Tensor, X: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
     op, ldo = _rows("out", out, Y.dtype, M, N, dev)
     xp, ldx = _rows("X", X, torch.bfloat16, M, K, dev)
     bf16, i32 = torch.bfloat16, torch.int32
+    if workspace is None:   # of this call alone: calls on other streams and captured graphs have their own
+        need = lora_workspace_bytes(M, r, L, _ROWS_DTYPE[Y.dtype])
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
     _call("macaq_lora_add", dev, yp, ldy, op, ldo, _ROWS_DTYPE[Y.dtype], xp, ldx, M, K, N,
           _arg("A", A, bf16, (L, r, K), dev), _arg("B", B, bf16, (L, N, r), dev), r, L,
           None if scale is None else _arg("scale", scale, torch.float32, (L,), dev),
           _arg("group_offsets", group_offsets, i32, (L + 1,), dev),
-          None if row_index is None else _arg("row_index", row_index, i32, (M,), dev))
+          None if row_index is None else _arg("row_index", row_index, i32, (M,), dev),
+          None if workspace is None else _arg("workspace", workspace, torch.uint8, workspace.shape, dev),
+          0 if workspace is None else workspace.numel())
     return out
 
 

@@ -4,11 +4,14 @@
 //
 // Bound by HBM: for a prefill by Y in and out, for a decode batch by the active adapters' A and B; for a few rows by latency.
 //
-// One launch. A cluster of eight CTAs takes a chunk of up to 16 or 64 rows of one adapter (rows of no adapter are chunks of
-// their own, copied when out is not Y). Each CTA computes the chunk's V = X A^T over an eighth of K; the partial sums are
-// added through distributed shared memory (each CTA adds an eighth of V and sends it to all), and each CTA then adds
-// V B^T to an eighth of the columns. A and B are read once per chunk, V never leaves the chip, and while the first product
-// runs the CTA's part of B is already on its way into L2.
+// Few rows (kFused): one launch. A cluster of eight CTAs takes a chunk of up to 16 or 64 rows of one adapter (rows of no
+// adapter are chunks of their own, copied when out is not Y). Each CTA computes the chunk's V = X A^T over an eighth of K;
+// the partial sums are added through distributed shared memory (each CTA adds an eighth of V and sends it to all), and each
+// CTA then adds V B^T to its slice of the columns. With few chunks several clusters share one: each makes V for itself and
+// has a part of the columns. While the first product runs the CTA's part of B is already on its way into L2.
+// Many rows: two launches (kShrink, kExpand), because whole clusters of eight leave SMs idle at the end of a long launch.
+// The first ends with V, in the form the second product takes it, in the workspace; the second takes (chunk, slice of
+// the columns) per CTA without clusters and has its first loads of Y and B under way while the first drains.
 //
 // Both products are bf16 MMAs (m16n8k16) fed straight from global memory: lane (g, t) takes 16 bytes, 8 neighbouring k of
 // row g at 8 t of a 32-wide k step, and the two MMAs of the step take their halves; both operands use the same order, so
@@ -29,6 +32,7 @@ constexpr int kLoraThreads = 256;
 constexpr int kLoraWarps = kLoraThreads / 32;
 constexpr int kLoraCluster = 8;
 constexpr int kLoraMaxRank = 128;
+enum LoraMode { kFused, kShrink, kExpand };
 
 struct LoraArgs {
     const void *y;            // [M, N], rows ldy apart
@@ -41,6 +45,8 @@ struct LoraArgs {
     const int32_t *row_index; // [M] or nullptr: rows are sorted already
     int64_t ldy, ldo, ldx, M, N, K;
     int32_t r, L, f32;
+    uint16_t *v;              // workspace (two launches): V per chunk, [part][row][stride]
+    int32_t slices;           // of the columns, per chunk
 };
 
 // Shared memory for rank r, chunks of 16 mt rows and `parts` bf16 parts of V: the CTA's partial V per k split, its sum, the
@@ -49,9 +55,10 @@ __host__ __device__ constexpr int lora_padded_rank(int r) { return r <= 32 ? 32 
 __host__ __device__ constexpr int lora_v_stride(int r) {   // bf16; 64 bytes off a multiple of 128: no bank conflicts
     return lora_padded_rank(r) == 32 ? 32 : lora_padded_rank(r) + 32;
 }
-__host__ __device__ constexpr int lora_splits(int mt) { return kLoraWarps / mt; }
-__host__ __device__ constexpr int lora_smem_bytes(int r, int mt, int parts) {
-    return (lora_splits(mt) + 1) * 16 * mt * r * 4 + parts * 16 * mt * lora_v_stride(r) * 2;
+__host__ __device__ constexpr int lora_splits(int mt) { return mt == 4 ? kLoraWarps / 2 : kLoraWarps / mt; }
+__host__ __device__ constexpr int lora_v_bytes(int r, int mt, int parts) { return parts * 16 * mt * lora_v_stride(r) * 2; }
+__host__ __device__ constexpr int lora_smem_bytes(int r, int mt, int parts, LoraMode mode) {
+    return (mode == kExpand ? 0 : (lora_splits(mt) + 1) * 16 * mt * r * 4) + (mode == kShrink ? 0 : lora_v_bytes(r, mt, parts));
 }
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -139,22 +146,27 @@ struct LoraPiece {
 };
 
 // Grid: one cluster per chunk. kMt: m16 tiles of a chunk; kSteps: 32-wide steps of the rank.
-template <int kMt, int kSteps, bool kF32>
+template <int kMt, int kSteps, bool kF32, LoraMode kMode>
 __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
     constexpr int kRows = 16 * kMt, kSplits = lora_splits(kMt), kParts = kF32 ? 3 : 2, kElement = kF32 ? 4 : 2;
     extern __shared__ __align__(16) uint8_t s_lora[];
     __shared__ int32_t s_off[kRouteMaxExperts + 2];
     __shared__ int64_t s_row[kRows];                // row of X, Y and out, -1: none
     __shared__ int64_t s_y[kRows], s_out[kRows];    // their offsets in Y and out in bytes
-    griddep_wait();
+    // The first launch of two waits for everything before it and only then lets the second start, so the plan, Y and B are
+    // complete for both; the second waits for V.
+    if constexpr (kMode != kExpand) griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int rank = blockIdx.x % kLoraCluster;
-    const LoraChunk ch = lora_find_chunk(p, blockIdx.x / kLoraCluster, kRows, s_off);
-    if (ch.rows == 0 || (ch.a == p.L && p.out == p.y)) return;   // the same for the whole cluster
+    const int rank = blockIdx.x % kLoraCluster, z = blockIdx.x / p.slices, slice = blockIdx.x % p.slices;
+    const LoraChunk ch = lora_find_chunk(p, z, kRows, s_off);
+    if (ch.rows == 0 || (ch.a == p.L && (kMode == kShrink || p.out == p.y))) {   // the same for the whole cluster
+        if constexpr (kMode == kExpand) griddep_wait();
+        return;
+    }
     const int r = p.r;
     // this CTA's columns, in steps of 32, and k steps of 32
-    const int64_t nsteps = (p.N + 31) / 32, n_begin = nsteps * rank / kLoraCluster, n_end = nsteps * (rank + 1) / kLoraCluster;
+    const int64_t nsteps = (p.N + 31) / 32, n_begin = nsteps * slice / p.slices, n_end = nsteps * (slice + 1) / p.slices;
     const int64_t ksteps = (p.K + 31) / 32, k_begin = ksteps * rank / kLoraCluster, k_end = ksteps * (rank + 1) / kLoraCluster;
     for (int i = threadIdx.x; i < kRows; i += kLoraThreads) {
         int64_t m = -1;
@@ -166,6 +178,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
     __syncthreads();
 
     if (ch.a == p.L) {   // rows of no adapter
+        if constexpr (kMode == kExpand) griddep_wait();   // out may still be in use
         const int64_t per = (n_end - n_begin) * 4;
         for (int64_t i = threadIdx.x; i < ch.rows * per; i += kLoraThreads) {
             const int64_t m = s_row[i / per], n = n_begin * 32 + i % per * 8;
@@ -177,59 +190,75 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
     }
 
     const uint16_t *A = p.A + static_cast<int64_t>(ch.a) * r * p.K, *B = p.B + static_cast<int64_t>(ch.a) * p.N * r;
-    {   // this CTA's part of B, towards L2
+    float *part = reinterpret_cast<float *>(s_lora);                  // [split][row][r]
+    float *mine = part + (kMode == kExpand ? 0 : kSplits * kRows * r);  // [row][r]
+    const int vs = lora_v_stride(r);
+    uint16_t *v_s = reinterpret_cast<uint16_t *>(mine + (kMode == kExpand ? 0 : kRows * r));   // [part][row][vs]
+    if constexpr (kMode == kFused) {   // this CTA's part of B, towards L2
         const char *from = reinterpret_cast<const char *>(B + n_begin * 32 * r);
         const int64_t bytes = (min(n_end * 32, p.N) - n_begin * 32) * r * 2;
         for (int64_t i = threadIdx.x * 128; i < bytes; i += kLoraThreads * 128)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(from + i));
     }
 
-    // V = X A^T: a warp takes one m16 tile and every kSplits-th k step of the CTA's part
-    float *part = reinterpret_cast<float *>(s_lora), *mine = part + kSplits * kRows * r;   // [split][row][r], [row][r]
-    uint16_t *v_s = reinterpret_cast<uint16_t *>(mine + kRows * r);                       // [part][row][stride]
-    const int vs = lora_v_stride(r);
-    {
-        const int mt = warp % kMt, split = warp / kMt;
-        const int64_t row_lo = s_row[16 * mt + g], row_hi = s_row[16 * mt + g + 8];
-        const uint16_t *x_lo = p.x + row_lo * p.ldx + 8 * t, *x_hi = p.x + row_hi * p.ldx + 8 * t;
+    if constexpr (kMode != kExpand) {
+        // V = X A^T: a warp takes one or two m16 tiles and every kSplits-th k step of the CTA's part
+        constexpr int kMp = kMt == 4 ? 2 : 1;
+        const int m0 = warp % (kMt / kMp) * kMp, split = warp / (kMt / kMp);
+        const uint16_t *x_row[kMp][2];
+#pragma unroll
+        for (int mt = 0; mt < kMp; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t m = s_row[16 * (m0 + mt) + 8 * h + g];
+                x_row[mt][h] = m < 0 ? nullptr : p.x + m * p.ldx + 8 * t;
+            }
         constexpr int kTiles = kSteps == 1 ? 4 : 8;   // n8 tiles of V at a time
+        constexpr int kUnroll = kMp == 1 ? 2 : 1;
         for (int j0 = 0; j0 < r; j0 += 8 * kTiles) {
-            float acc[kTiles][4] = {};
-#pragma unroll 2
+            float acc[kMp][kTiles][4] = {};
+#pragma unroll kUnroll
             for (int64_t s = k_begin + split; s < k_end; s += kSplits) {
                 const int64_t k = s * 32;
                 const bool on = k + 8 * t < p.K;
-                const uint4 lo = lora_ld(x_lo + k, on && row_lo >= 0), hi = lora_ld(x_hi + k, on && row_hi >= 0);
-                uint4 b[kTiles];
+                uint4 x[kMp][2], b[kTiles];
+#pragma unroll
+                for (int mt = 0; mt < kMp; ++mt)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) x[mt][h] = lora_ld(x_row[mt][h] + k, on && x_row[mt][h] != nullptr);
 #pragma unroll
                 for (int j = 0; j < kTiles; ++j)
                     b[j] = lora_ld(A + static_cast<int64_t>(j0 + 8 * j + g) * p.K + k + 8 * t, on && j0 + 8 * j < r);
 #pragma unroll
-                for (int j = 0; j < kTiles; ++j) {
-                    mma_bf16(acc[j], lo.x, hi.x, lo.y, hi.y, b[j].x, b[j].y);
-                    mma_bf16(acc[j], lo.z, hi.z, lo.w, hi.w, b[j].z, b[j].w);
-                }
+                for (int mt = 0; mt < kMp; ++mt)
+#pragma unroll
+                    for (int j = 0; j < kTiles; ++j) {
+                        mma_bf16(acc[mt][j], x[mt][0].x, x[mt][1].x, x[mt][0].y, x[mt][1].y, b[j].x, b[j].y);
+                        mma_bf16(acc[mt][j], x[mt][0].z, x[mt][1].z, x[mt][0].w, x[mt][1].w, b[j].z, b[j].w);
+                    }
             }
 #pragma unroll
-            for (int j = 0; j < kTiles; ++j)
-                if (j0 + 8 * j < r) {
-                    float *dst = part + (split * kRows + 16 * mt + g) * r + j0 + 8 * j + 2 * t;
-                    *reinterpret_cast<float2 *>(dst) = make_float2(acc[j][0], acc[j][1]);
-                    *reinterpret_cast<float2 *>(dst + 8 * r) = make_float2(acc[j][2], acc[j][3]);
-                }
-        }
-    }
-    // the parts' columns past r are zero
-    for (int i = threadIdx.x; i < kParts * kRows * (lora_padded_rank(r) - r); i += kLoraThreads) {
-        const int per = lora_padded_rank(r) - r;
-        v_s[i / per * vs + r + i % per] = 0;
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < kRows * r; i += kLoraThreads) {
-        float v = 0.0f;
+            for (int mt = 0; mt < kMp; ++mt)
 #pragma unroll
-        for (int s = 0; s < kSplits; ++s) v += part[s * kRows * r + i];
-        mine[i] = v;
+                for (int j = 0; j < kTiles; ++j)
+                    if (j0 + 8 * j < r) {
+                        float *dst = part + (split * kRows + 16 * (m0 + mt) + g) * r + j0 + 8 * j + 2 * t;
+                        *reinterpret_cast<float2 *>(dst) = make_float2(acc[mt][j][0], acc[mt][j][1]);
+                        *reinterpret_cast<float2 *>(dst + 8 * r) = make_float2(acc[mt][j][2], acc[mt][j][3]);
+                    }
+        }
+        if constexpr (kMode == kFused)   // the parts' columns past r are zero
+            for (int i = threadIdx.x; i < kParts * kRows * (lora_padded_rank(r) - r); i += kLoraThreads) {
+                const int per = lora_padded_rank(r) - r;
+                v_s[i / per * vs + r + i % per] = 0;
+            }
+        __syncthreads();
+        for (int i = threadIdx.x; i < kRows * r; i += kLoraThreads) {
+            float v = 0.0f;
+#pragma unroll
+            for (int s = 0; s < kSplits; ++s) v += part[s * kRows * r + i];
+            mine[i] = v;
+        }
     }
     // The second product's loads. A warp takes every eighth 32-column step, kBatch of them at a time; the first batch sets out
     // here, before V is complete. Logical column c of n8 tile i is column 8 (c / 2) + 2 i + c % 2 of the step.
@@ -260,9 +289,11 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
                                           step < s_end && step * 32 + n_lane + 2 * i < N && 32 * ks + 8 * t < r);
         }
     };
-    load_batch();
-    cluster_sync();
-    {   // entries in pairs, an eighth of them per CTA: sum over the cluster, times scale, to everybody in bf16 parts
+    if constexpr (kMode != kShrink) load_batch();
+    if constexpr (kMode != kExpand) {
+        // entries in pairs, an eighth of them per CTA: sum over the cluster, times scale, in bf16 parts to every CTA of the
+        // cluster or to the workspace
+        cluster_sync();
         const float scale = p.scale ? __ldg(p.scale + ch.a) : 1.0f;
         const int pairs = kRows * r / 2;
         for (int i = rank * pairs / kLoraCluster + threadIdx.x; i < (rank + 1) * pairs / kLoraCluster; i += kLoraThreads) {
@@ -282,18 +313,33 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
             for (int k = 0; k < kParts; ++k) {   // each part is the rounding of what the ones before leave
                 const __nv_bfloat162 b = __floats2bfloat162_rn(v0, v1);
                 const uint32_t w = *reinterpret_cast<const uint32_t *>(&b);
-                v0 -= __uint_as_float(w << 16), v1 -= __uint_as_float(w & 0xFFFF0000u);
+                const float h0 = __uint_as_float(w << 16), h1 = __uint_as_float(w & 0xFFFF0000u);
+                v0 = isinf(h0) ? 0.0f : v0 - h0, v1 = isinf(h1) ? 0.0f : v1 - h1;   // an infinity stays one
+                const int at = (k * kRows + row) * vs + col;
+                if constexpr (kMode == kShrink) {
+                    *reinterpret_cast<uint32_t *>(p.v + static_cast<int64_t>(z) * kParts * kRows * vs + at) = w;
+                } else {
 #pragma unroll
-                for (int c = 0; c < kLoraCluster; ++c)
-                    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
-                                     map_to_rank(smem_u32(v_s + (k * kRows + row) * vs + col), c)),
-                                 "r"(w)
-                                 : "memory");
+                    for (int c = 0; c < kLoraCluster; ++c)
+                        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to_rank(smem_u32(v_s + at), c)), "r"(w)
+                                     : "memory");
+                }
             }
         }
+        __syncwarp();
+        cluster_sync();   // V is complete; and no CTA leaves while another reads its sums
+        if constexpr (kMode == kShrink) return;
+    } else {
+        griddep_wait();
+        const uint4 *src = reinterpret_cast<const uint4 *>(p.v + static_cast<int64_t>(z) * kParts * kRows * vs);
+        const int per_row = vs / 8;
+        for (int i = threadIdx.x; i < kParts * kRows * per_row; i += kLoraThreads) {
+            uint4 w = __ldcg(src + i);
+            if (i % per_row * 8 >= r) w = make_uint4(0u, 0u, 0u, 0u);   // past the rank nothing was written
+            reinterpret_cast<uint4 *>(v_s)[i] = w;
+        }
+        __syncthreads();
     }
-    __syncwarp();
-    cluster_sync();
 
     // out = Y + V B^T, all rows of 32 columns at a time, tile by tile of 16 rows
 #pragma unroll 1

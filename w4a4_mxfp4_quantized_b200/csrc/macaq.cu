@@ -14,6 +14,7 @@
 #include <map>
 #include <mutex>
 #include <tuple>
+#include <type_traits>
 
 #include "macaq.h"
 #include "flip.cuh"
@@ -1208,26 +1209,57 @@ macaq_status moe_w4a16(const MoeArgs &a, void *workspace, size_t ws_bytes, cudaS
 }
 
 // ------------------------------------------------------------------------ low-rank adapters
-template <int kMt, int kSteps, bool kF32>
-macaq_status run_lora_steps(const LoraArgs &g, cudaStream_t st) {
-    auto k = lora_add_kernel<kMt, kSteps, kF32>;
-    const size_t smem = lora_smem_bytes(g.r, kMt, kF32 ? 3 : 2);
+constexpr int64_t kLoraFusedChunks = 16;   // wide chunks that one launch takes
+
+// How a call is cut: 64-row chunks once adapters have some (A and B are read per chunk); two launches once the chunks alone
+// fill the GPU.
+struct LoraPlan {
+    bool wide, two;
+    int64_t chunks;
+    size_t ws_bytes;
+};
+
+LoraPlan lora_plan(int64_t M, int32_t L, int32_t r, bool f32) {
+    LoraPlan p;
+    p.wide = M > 32 * static_cast<int64_t>(L);
+    const int rows = p.wide ? 64 : 16;
+    // one chunk per adapter with rows and one for the rows of none, one more per `rows` rows
+    p.chunks = std::min<int64_t>(L + 1, M) + M / rows;
+    p.two = p.wide && p.chunks > kLoraFusedChunks;
+    p.ws_bytes = p.two ? static_cast<size_t>(p.chunks) * lora_v_bytes(r, 4, f32 ? 3 : 2) : 0;
+    return p;
+}
+
+template <int kMt, int kSteps, bool kF32, LoraMode kMode>
+macaq_status launch_lora(LoraArgs g, int64_t chunks, int slices, cudaStream_t st) {
+    auto k = lora_add_kernel<kMt, kSteps, kF32, kMode>;
+    const size_t smem = lora_smem_bytes(g.r, kMt, kF32 ? 3 : 2, kMode);
     macaq_status s = set_smem(k, smem);
     if (s != MACAQ_OK) return s;
-    // chunks: one per adapter with rows and one for the rows of none, one more per 16 kMt rows
-    const int64_t chunks = std::min<int64_t>(g.L + 1, g.M) + g.M / (16 * kMt);
-    if (chunks * kLoraCluster >= (int64_t(1) << 31)) return MACAQ_ERR_SHAPE;
-    return launch(k, dim3(static_cast<unsigned>(chunks * kLoraCluster)), dim3(kLoraThreads), smem, st, kLoraCluster, g);
+    g.slices = slices;
+    if (chunks * slices >= (int64_t(1) << 31)) return MACAQ_ERR_SHAPE;
+    return launch(k, dim3(static_cast<unsigned>(chunks * slices)), dim3(kLoraThreads), smem, st,
+                  kMode == kExpand ? 1 : kLoraCluster, g);
 }
 
-template <int kMt, bool kF32>
-macaq_status run_lora(const LoraArgs &g, cudaStream_t st) {
-    if (g.r <= 32) return run_lora_steps<kMt, 1, kF32>(g, st);
-    if (g.r <= 64) return run_lora_steps<kMt, 2, kF32>(g, st);
-    return run_lora_steps<kMt, 4, kF32>(g, st);
+template <int kSteps, bool kF32>
+macaq_status run_lora(const LoraArgs &g, const LoraPlan &p, int sms, cudaStream_t st) {
+    const int64_t nsteps = (g.N + 31) / 32;
+    if (p.two) {
+        macaq_status s = launch_lora<4, kSteps, kF32, kShrink>(g, p.chunks, kLoraCluster, st);
+        if (s != MACAQ_OK) return s;
+        // slices of at least one step per warp, for about four CTAs per SM
+        const int64_t slices = std::max<int64_t>(1, std::min<int64_t>(nsteps / kLoraWarps, (4 * sms + p.chunks - 1) / p.chunks));
+        return launch_lora<4, kSteps, kF32, kExpand>(g, p.chunks, static_cast<int>(slices), st);
+    }
+    // clusters that share a chunk: while SMs are left, and every warp has a step
+    const int64_t share = std::max<int64_t>(1, std::min<int64_t>(2 * sms / (kLoraCluster * p.chunks), nsteps / (kLoraCluster * kLoraWarps)));
+    const int slices = static_cast<int>(share) * kLoraCluster;
+    return p.wide ? launch_lora<4, kSteps, kF32, kFused>(g, p.chunks, slices, st)
+                  : launch_lora<1, kSteps, kF32, kFused>(g, p.chunks, slices, st);
 }
 
-macaq_status lora_add(const LoraArgs &p, int32_t dtype, cudaStream_t st) {
+macaq_status lora_add(const LoraArgs &p, int32_t dtype, void *workspace, size_t ws_bytes, cudaStream_t st) {
     constexpr int64_t kMax = int64_t(1) << 31;
     if (p.M < 0 || p.M >= kMax || p.K <= 0 || p.K >= kMax || p.N <= 0 || p.N >= kMax || p.K % 8 || p.N % 8 || p.r < 8 ||
         p.r > kLoraMaxRank || p.r % 8 || p.L < 1 || p.L > kRouteMaxExperts)
@@ -1241,17 +1273,24 @@ macaq_status lora_add(const LoraArgs &p, int32_t dtype, cudaStream_t st) {
     if (p.y == nullptr || p.out == nullptr || p.x == nullptr || p.A == nullptr || p.B == nullptr || p.offsets == nullptr)
         return MACAQ_ERR_INVALID_ARG;
     if (!aligned16(p.y) || !aligned16(p.out) || !aligned16(p.x) || !aligned16(p.A) || !aligned16(p.B) || !aligned16(p.offsets) ||
-        !aligned16(p.row_index) || !aligned4(p.scale))
+        !aligned16(p.row_index) || !aligned4(p.scale) || !aligned16(workspace))
         return MACAQ_ERR_ALIGNMENT;
+    const bool f32 = dtype == MACAQ_OUT_F32;
+    const LoraPlan plan = lora_plan(p.M, p.L, p.r, f32);
+    if (plan.ws_bytes > 0 && (workspace == nullptr || ws_bytes < plan.ws_bytes)) return MACAQ_ERR_WORKSPACE;
     DeviceInfo dev;
     macaq_status s = device_info(&dev);
     if (s != MACAQ_OK) return s;
     LoraArgs g = p;
-    g.f32 = dtype == MACAQ_OUT_F32;
-    // 64-row chunks once adapters have some: A and B are read per chunk
-    const bool wide = p.M > 32 * static_cast<int64_t>(p.L);
-    if (g.f32) return wide ? run_lora<4, true>(g, st) : run_lora<1, true>(g, st);
-    return wide ? run_lora<4, false>(g, st) : run_lora<1, false>(g, st);
+    g.f32 = f32;
+    g.v = static_cast<uint16_t *>(workspace);
+    auto run = [&](auto f) {
+        constexpr bool kF32 = decltype(f)::value;
+        if (g.r <= 32) return run_lora<1, kF32>(g, plan, dev.sms, st);
+        if (g.r <= 64) return run_lora<2, kF32>(g, plan, dev.sms, st);
+        return run_lora<4, kF32>(g, plan, dev.sms, st);
+    };
+    return f32 ? run(std::true_type{}) : run(std::false_type{});
 }
 
 }  // namespace macaq
@@ -1485,8 +1524,8 @@ macaq_status macaq_moe_w4a16(const void *X, int64_t T, int64_t K, const float *w
 
 macaq_status macaq_lora_add(const void *Y, int64_t ldy, void *out, int64_t ldo, int32_t dtype, const void *X, int64_t ldx,
                             int64_t M, int64_t K, int64_t N, const void *A, const void *B, int32_t r, int32_t L,
-                            const float *scale, const int32_t *group_offsets, const int32_t *row_index,
-                            macaq_stream_t stream) {
+                            const float *scale, const int32_t *group_offsets, const int32_t *row_index, void *workspace,
+                            size_t ws_bytes, macaq_stream_t stream) {
     macaq::LoraArgs p{};
     p.y = Y;
     p.out = out;
@@ -1504,7 +1543,13 @@ macaq_status macaq_lora_add(const void *Y, int64_t ldy, void *out, int64_t ldo, 
     p.K = K;
     p.r = r;
     p.L = L;
-    return macaq::lora_add(p, dtype, static_cast<cudaStream_t>(stream));
+    return macaq::lora_add(p, dtype, workspace, ws_bytes, static_cast<cudaStream_t>(stream));
+}
+
+size_t macaq_lora_workspace_bytes(int64_t M, int32_t r, int32_t L, int32_t dtype) {
+    if (M <= 0 || M >= (int64_t(1) << 31) || L < 1 || L > macaq::kRouteMaxExperts || r < 8 || r > macaq::kLoraMaxRank || r % 8)
+        return 0;
+    return macaq::lora_plan(M, L, r, dtype == MACAQ_OUT_F32).ws_bytes;
 }
 
 }  // extern "C"
