@@ -16,13 +16,15 @@
 // Both products are bf16 MMAs (m16n8k16) fed straight from global memory: lane (g, t) takes 16 bytes, 8 neighbouring k of
 // row g at 8 t of a 32-wide k step, and the two MMAs of the step take their halves; both operands use the same order, so
 // the sum over k is complete. In the second product the 32 columns of a step are dealt to the four n8 tiles so that a lane
-// ends up with 8 neighbouring columns of a row: Y moves in 16-byte pieces. V is held as two bf16 parts (16 bits) for
+// ends up with 8 neighbouring columns of a row: Y moves in 16-byte pieces, through a ring of cp.async stages in which each
+// lane reads back what it copied itself (no barrier; the copies of the next steps are in flight while one is added). V is held as two bf16 parts (16 bits) for
 // bf16 outputs and three (24 bits, all of fp32) for fp32, so it is not what limits the result.
 #pragma once
 
 #include <cuda_bf16.h>
 
 #include "groups.cuh"
+#include "moe_w4a16.cuh"
 #include "ptx.cuh"
 #include "route.cuh"
 
@@ -57,8 +59,28 @@ __host__ __device__ constexpr int lora_v_stride(int r) {   // bf16; 64 bytes off
 }
 __host__ __device__ constexpr int lora_splits(int mt) { return mt == 4 ? kLoraWarps / 2 : kLoraWarps / mt; }
 __host__ __device__ constexpr int lora_v_bytes(int r, int mt, int parts) { return parts * 16 * mt * lora_v_stride(r) * 2; }
-__host__ __device__ constexpr int lora_smem_bytes(int r, int mt, int parts, LoraMode mode) {
-    return (mode == kExpand ? 0 : (lora_splits(mt) + 1) * 16 * mt * r * 4) + (mode == kShrink ? 0 : lora_v_bytes(r, mt, parts));
+// The ring of the second product: 16-byte pieces per lane and stage (Y of all rows; for one m16 tile B too), and stages.
+__host__ __device__ constexpr int lora_ring_pieces(int mt, int steps, bool f32) {
+    return mt * 2 * (f32 ? 2 : 1) + (mt == 1 ? 4 * steps : 0);
+}
+__host__ __device__ constexpr int lora_ring_stages(int mt, int steps, bool f32) { return mt == 1 && steps == 1 ? (f32 ? 3 : 4) : 2; }
+__host__ __device__ constexpr int lora_ring_bytes(int mt, int steps, bool f32) {
+    return kLoraWarps * lora_ring_stages(mt, steps, f32) * lora_ring_pieces(mt, steps, f32) * 512;
+}
+// Offsets: [ring, over the partial sums][the CTA's sum][parts of V]
+__host__ __device__ constexpr int lora_sum_offset(int r, int mt, int steps, bool f32, LoraMode mode) {
+    const int part = mode == kExpand ? 0 : lora_splits(mt) * 16 * mt * r * 4, ring = mode == kShrink ? 0 : lora_ring_bytes(mt, steps, f32);
+    return part > ring ? part : ring;
+}
+__host__ __device__ constexpr int lora_v_offset(int r, int mt, int steps, bool f32, LoraMode mode) {
+    return lora_sum_offset(r, mt, steps, f32, mode) + (mode == kExpand ? 0 : 16 * mt * r * 4);
+}
+__host__ __device__ constexpr int lora_smem_bytes(int r, int mt, int steps, bool f32, LoraMode mode) {
+    return lora_v_offset(r, mt, steps, f32, mode) + (mode == kShrink ? 0 : lora_v_bytes(r, mt, f32 ? 3 : 2));
+}
+
+__device__ __forceinline__ void lora_copy16(uint32_t dst, const void *src, bool on) {   // off: zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -190,10 +212,10 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
     }
 
     const uint16_t *A = p.A + static_cast<int64_t>(ch.a) * r * p.K, *B = p.B + static_cast<int64_t>(ch.a) * p.N * r;
-    float *part = reinterpret_cast<float *>(s_lora);                  // [split][row][r]
-    float *mine = part + (kMode == kExpand ? 0 : kSplits * kRows * r);  // [row][r]
+    float *part = reinterpret_cast<float *>(s_lora);                                                   // [split][row][r]
+    float *mine = reinterpret_cast<float *>(s_lora + lora_sum_offset(r, kMt, kSteps, kF32, kMode));     // [row][r]
     const int vs = lora_v_stride(r);
-    uint16_t *v_s = reinterpret_cast<uint16_t *>(mine + (kMode == kExpand ? 0 : kRows * r));   // [part][row][vs]
+    uint16_t *v_s = reinterpret_cast<uint16_t *>(s_lora + lora_v_offset(r, kMt, kSteps, kF32, kMode));  // [part][row][vs]
     if constexpr (kMode == kFused) {   // this CTA's part of B, towards L2
         const char *from = reinterpret_cast<const char *>(B + n_begin * 32 * r);
         const int64_t bytes = (min(n_end * 32, p.N) - n_begin * 32) * r * 2;
@@ -260,36 +282,51 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
             mine[i] = v;
         }
     }
-    // The second product's loads. A warp takes every eighth 32-column step, kBatch of them at a time; the first batch sets out
-    // here, before V is complete. Logical column c of n8 tile i is column 8 (c / 2) + 2 i + c % 2 of the step.
-    constexpr int kBatch = kMt > 1 || kSteps == 4 ? 1 : (kSteps == 1 && !kF32 ? 4 : 2);
+    // The second product's loads. A warp takes every eighth 32-column step; the first copies set out here, before V is complete.
+    // Logical column c of n8 tile i is column 8 (c / 2) + 2 i + c % 2 of the step.
+    constexpr int kStages = lora_ring_stages(kMt, kSteps, kF32), kPieces = lora_ring_pieces(kMt, kSteps, kF32);
+    constexpr int kYPieces = kF32 ? 2 : 1;   // of a lane's eight columns
     const int N = static_cast<int>(p.N), s_end = static_cast<int>(n_end), n_lane = 8 * (g >> 1) + (g & 1);
     int s = static_cast<int>(n_begin) + warp;
-    uint4 b[kBatch][kSteps][4];
-    LoraPiece<kF32> y[kMt > 1 ? 2 : kBatch][2];
     const uint16_t *b_lane = B + static_cast<int64_t>(n_lane) * r + 8 * t;
-    auto load_y = [&](int step, int mt, LoraPiece<kF32> (&to)[2]) {
+    uint8_t *ring = s_lora + (warp * kStages * kPieces * 32 + lane) * 16;   // this lane's piece 0 of stage 0
+    auto b_on = [&](int step, int ks, int i) { return step < s_end && step * 32 + n_lane + 2 * i < N && 32 * ks + 8 * t < r; };
+    auto b_at = [&](int step, int ks, int i) { return b_lane + (static_cast<int64_t>(step) * 32 + 2 * i) * r + 32 * ks; };
+    auto issue = [&](int step, int stage) {
+        const uint32_t dst = smem_u32(ring) + stage * kPieces * 512;
+        if (step < s_end) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int row = 16 * mt + 8 * h + g;
-            to[h].load(static_cast<const char *>(p.y) + s_y[row] + (step * 32 + 8 * t) * kElement,
-                       s_row[row] >= 0 && step * 32 + 8 * t < N);
+            for (int k = 0; k < 2 * kMt; ++k) {
+                const int row = 8 * k + g;
+                if (s_row[row] >= 0 && step * 32 + 8 * t < N) {
+                    const char *src = static_cast<const char *>(p.y) + s_y[row] + (step * 32 + 8 * t) * kElement;
+#pragma unroll
+                    for (int c = 0; c < kYPieces; ++c) lora_copy16(dst + (k * kYPieces + c) * 512, src + 16 * c, true);
+                }
+            }
+            if constexpr (kMt == 1) {
+#pragma unroll
+                for (int k = 0; k < 4 * kSteps; ++k) {
+                    const bool on = b_on(step, k / 4, k % 4);
+                    lora_copy16(dst + (2 * kYPieces + k) * 512, on ? b_at(step, k / 4, k % 4) : B, on);
+                }
+            }
         }
+        cp_async_commit();   // an empty group keeps groups and steps in step
     };
-    auto load_batch = [&] {
+    uint4 b[kSteps][4], b_next[kSteps][4];   // kMt > 1: B in registers, the next step's on its way while one is multiplied
+    auto load_b = [&](int step, uint4 (&to)[kSteps][4]) {
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int step = s + u * kLoraWarps;
-            if (step < s_end) load_y(step, 0, y[kMt > 1 ? 0 : u]);
+        for (int ks = 0; ks < kSteps; ++ks)
 #pragma unroll
-            for (int ks = 0; ks < kSteps; ++ks)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    b[u][ks][i] = lora_ld(b_lane + (static_cast<int64_t>(step) * 32 + 2 * i) * r + 32 * ks,
-                                          step < s_end && step * 32 + n_lane + 2 * i < N && 32 * ks + 8 * t < r);
-        }
+            for (int i = 0; i < 4; ++i) to[ks][i] = lora_ld(b_at(step, ks, i), b_on(step, ks, i));
     };
-    if constexpr (kMode != kShrink) load_batch();
+    if constexpr (kMode != kShrink) {
+        if constexpr (kMode == kFused) __syncthreads();   // the partial sums are read: the ring lies over them
+#pragma unroll
+        for (int k = 0; k < kStages - 1; ++k) issue(s + k * kLoraWarps, k);
+        if constexpr (kMt > 1) load_b(s, b);
+    }
     if constexpr (kMode != kExpand) {
         // entries in pairs, an eighth of them per CTA: sum over the cluster, times scale, in bf16 parts to every CTA of the
         // cluster or to the workspace
@@ -342,47 +379,57 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
     }
 
     // out = Y + V B^T, all rows of 32 columns at a time, tile by tile of 16 rows
+    int stage = 0;
 #pragma unroll 1
-    for (;;) {
+    for (; s < s_end; s += kLoraWarps) {
+        issue(s + (kStages - 1) * kLoraWarps, stage == 0 ? kStages - 1 : stage - 1);
+        if constexpr (kMt > 1 && kSteps < 4) load_b(s + kLoraWarps, b_next);
+        cp_async_wait<kStages - 1>();   // this lane's copies of the step have landed
+        const uint4 *piece = reinterpret_cast<const uint4 *>(ring + stage * kPieces * 512);
+        stage = stage == kStages - 1 ? 0 : stage + 1;
+        if constexpr (kMt == 1) {
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int step = s + u * kLoraWarps;
-            if (step >= s_end) break;
+            for (int k = 0; k < 4 * kSteps; ++k) b[k / 4][k % 4] = piece[(2 * kYPieces + k) * 32];
+        }
 #pragma unroll
-            for (int mt = 0; mt < kMt; ++mt) {
-                if (16 * mt >= ch.rows) break;
-                if constexpr (kMt > 1) {   // the next tile's Y on its way
-                    if (mt + 1 < kMt) load_y(step, mt + 1, y[(mt + 1) & 1]);
+        for (int mt = 0; mt < kMt; ++mt) {
+            if (16 * mt >= ch.rows) break;
+            float acc[4][4] = {};
+#pragma unroll
+            for (int ks = 0; ks < kSteps; ++ks)
+#pragma unroll
+                for (int q = 0; q < kParts; ++q) {
+                    const uint16_t *v = v_s + (q * kRows + 16 * mt + g) * vs + 32 * ks + 8 * t;
+                    const uint4 lo = *reinterpret_cast<const uint4 *>(v), hi = *reinterpret_cast<const uint4 *>(v + 8 * vs);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        mma_bf16(acc[i], lo.x, hi.x, lo.y, hi.y, b[ks][i].x, b[ks][i].y);
+                        mma_bf16(acc[i], lo.z, hi.z, lo.w, hi.w, b[ks][i].z, b[ks][i].w);
+                    }
                 }
-                LoraPiece<kF32>(&yt)[2] = y[kMt > 1 ? (mt & 1) : u];
-                float acc[4][4] = {};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float d[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[2 * i] = acc[i][2 * h], d[2 * i + 1] = acc[i][2 * h + 1];
+                const int row = 16 * mt + 8 * h + g;
+                LoraPiece<kF32> y;
+#pragma unroll
+                for (int c = 0; c < kYPieces; ++c) y.v[c] = piece[((2 * mt + h) * kYPieces + c) * 32];
+                y.add(d);
+                y.store(static_cast<char *>(p.out) + s_out[row] + (s * 32 + 8 * t) * kElement, s_row[row] >= 0 && s * 32 + 8 * t < N);
+            }
+        }
+        if constexpr (kMt > 1) {
+            if constexpr (kSteps < 4) {
 #pragma unroll
                 for (int ks = 0; ks < kSteps; ++ks)
 #pragma unroll
-                    for (int q = 0; q < kParts; ++q) {
-                        const uint16_t *v = v_s + (q * kRows + 16 * mt + g) * vs + 32 * ks + 8 * t;
-                        const uint4 lo = *reinterpret_cast<const uint4 *>(v), hi = *reinterpret_cast<const uint4 *>(v + 8 * vs);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            mma_bf16(acc[i], lo.x, hi.x, lo.y, hi.y, b[u][ks][i].x, b[u][ks][i].y);
-                            mma_bf16(acc[i], lo.z, hi.z, lo.w, hi.w, b[u][ks][i].z, b[u][ks][i].w);
-                        }
-                    }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float d[8];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) d[2 * i] = acc[i][2 * h], d[2 * i + 1] = acc[i][2 * h + 1];
-                    const int row = 16 * mt + 8 * h + g;
-                    yt[h].add(d);
-                    yt[h].store(static_cast<char *>(p.out) + s_out[row] + (step * 32 + 8 * t) * kElement,
-                                s_row[row] >= 0 && step * 32 + 8 * t < N);
-                }
+                    for (int i = 0; i < 4; ++i) b[ks][i] = b_next[ks][i];
+            } else {
+                load_b(s + kLoraWarps, b);
             }
         }
-        s += kBatch * kLoraWarps;
-        if (s >= s_end) break;
-        load_batch();
     }
 }
 

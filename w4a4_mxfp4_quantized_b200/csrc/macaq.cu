@@ -1233,7 +1233,7 @@ LoraPlan lora_plan(int64_t M, int32_t L, int32_t r, bool f32) {
 template <int kMt, int kSteps, bool kF32, LoraMode kMode>
 macaq_status launch_lora(LoraArgs g, int64_t chunks, int slices, cudaStream_t st) {
     auto k = lora_add_kernel<kMt, kSteps, kF32, kMode>;
-    const size_t smem = lora_smem_bytes(g.r, kMt, kF32 ? 3 : 2, kMode);
+    const size_t smem = lora_smem_bytes(g.r, kMt, kSteps, kF32, kMode);
     macaq_status s = set_smem(k, smem);
     if (s != MACAQ_OK) return s;
     g.slices = slices;
