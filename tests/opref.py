@@ -124,7 +124,8 @@ def moe_layer(X, weights, off, row_index, pos, layer):
 
 
 def lora(Y, X, A, B, scale, off, row_index, rounding):
-    """fp64 tensors; rounding: half a step of the output type. Returns (out, bound)."""
+    """fp64 tensors; rounding: half a step of the output type. Returns (out, bound): fp32 sums, X A^T in bf16 for bf16 outputs
+    (half a step of it, 2^-8 of each of its values) and in all of fp32's bits otherwise, the output's rounding."""
     out, bound = Y.clone(), torch.zeros_like(Y)
     K, r = X.shape[1], A.shape[1]
     for a in range(A.shape[0]):
@@ -133,7 +134,7 @@ def lora(Y, X, A, B, scale, off, row_index, rounding):
             continue
         x, s = X[rows], (scale[a] if scale is not None else 1.0)
         v, mag = x @ A[a].T, x.abs() @ A[a].abs().T
-        ev = 2 * (K / 16 + 16) * F32 * mag
+        ev = 2 * (K / 16 + 16) * F32 * mag + (BF16 * v.abs() if rounding == BF16 else 0.0)
         out[rows] += s * (v @ B[a].T)
         bound[rows] += abs(s) * (ev @ B[a].abs().T + 2 * (r + 8) * F32 * (v.abs() @ B[a].abs().T))
     return out, bound * (1 + rounding) + rounding * out.abs() + 2 * F32 * Y.abs() + 2.0 ** -133

@@ -17,8 +17,8 @@
 // row g at 8 t of a 32-wide k step, and the two MMAs of the step take their halves; both operands use the same order, so
 // the sum over k is complete. In the second product the 32 columns of a step are dealt to the four n8 tiles so that a lane
 // ends up with 8 neighbouring columns of a row: Y moves in 16-byte pieces, through a ring of cp.async stages in which each
-// lane reads back what it copied itself (no barrier; the copies of the next steps are in flight while one is added). V is held as two bf16 parts (16 bits) for
-// bf16 outputs and three (24 bits, all of fp32) for fp32, so it is not what limits the result.
+// lane reads back what it copied itself (no barrier; the copies of the next steps are in flight while one is added). V is held in
+// up to three bf16 parts (8, 16 or 24 bits).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -57,7 +57,11 @@ __host__ __device__ constexpr int lora_padded_rank(int r) { return r <= 32 ? 32 
 __host__ __device__ constexpr int lora_v_stride(int r) {   // bf16; 64 bytes off a multiple of 128: no bank conflicts
     return lora_padded_rank(r) == 32 ? 32 : lora_padded_rank(r) + 32;
 }
-__host__ __device__ constexpr int lora_splits(int mt) { return mt == 4 ? kLoraWarps / 2 : kLoraWarps / mt; }
+__host__ __device__ constexpr int lora_splits(int mt) { return kLoraWarps / mt; }
+// bf16 parts that V is held in: three for fp32 outputs; for bf16 outputs two, and one for chunks of 64 rows, where the
+// second costs a quarter of the launch (2048 rows of rank 64 on 14336 columns: 38 against 29 us) and V's rounding, 2^-9 of
+// the adapter's share, stays under the output's own.
+__host__ __device__ constexpr int lora_parts(int mt, bool f32) { return f32 ? 3 : (mt == 4 ? 1 : 2); }
 __host__ __device__ constexpr int lora_v_bytes(int r, int mt, int parts) { return parts * 16 * mt * lora_v_stride(r) * 2; }
 // The ring of the second product: 16-byte pieces per lane and stage (Y of all rows; for one m16 tile B too), and stages.
 __host__ __device__ constexpr int lora_ring_pieces(int mt, int steps, bool f32) {
@@ -76,7 +80,7 @@ __host__ __device__ constexpr int lora_v_offset(int r, int mt, int steps, bool f
     return lora_sum_offset(r, mt, steps, f32, mode) + (mode == kExpand ? 0 : 16 * mt * r * 4);
 }
 __host__ __device__ constexpr int lora_smem_bytes(int r, int mt, int steps, bool f32, LoraMode mode) {
-    return lora_v_offset(r, mt, steps, f32, mode) + (mode == kShrink ? 0 : lora_v_bytes(r, mt, f32 ? 3 : 2));
+    return lora_v_offset(r, mt, steps, f32, mode) + (mode == kShrink ? 0 : lora_v_bytes(r, mt, lora_parts(mt, f32)));
 }
 
 __device__ __forceinline__ void lora_copy16(uint32_t dst, const void *src, bool on) {   // off: zeros
@@ -145,19 +149,23 @@ struct LoraPiece {
 #pragma unroll
         for (int i = 0; i < (kF32 ? 2 : 1); ++i) v[i] = __ldcg(reinterpret_cast<const uint4 *>(y) + i);
     }
-    __device__ __forceinline__ void add(const float (&d)[8]) {
+    // columns 2 i and 2 i + 1: what their sums start from, and their results
+    __device__ __forceinline__ void start(int i, float &a, float &b) const {
         if constexpr (kF32) {
-            uint32_t *w = reinterpret_cast<uint32_t *>(v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) + d[i]);
+            a = b = 0.0f;
         } else {
-            uint32_t *w = reinterpret_cast<uint32_t *>(v);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(w[i] << 16) + d[2 * i],
-                                                               __uint_as_float(w[i] & 0xFFFF0000u) + d[2 * i + 1]);
-                w[i] = *reinterpret_cast<const uint32_t *>(&b);
-            }
+            const uint32_t w = reinterpret_cast<const uint32_t *>(v)[i];
+            a = __uint_as_float(w << 16), b = __uint_as_float(w & 0xFFFF0000u);
+        }
+    }
+    __device__ __forceinline__ void finish(int i, float a, float b) {
+        uint32_t *w = reinterpret_cast<uint32_t *>(v);
+        if constexpr (kF32) {
+            w[2 * i] = __float_as_uint(__uint_as_float(w[2 * i]) + a);
+            w[2 * i + 1] = __float_as_uint(__uint_as_float(w[2 * i + 1]) + b);
+        } else {
+            const __nv_bfloat162 o = __floats2bfloat162_rn(a, b);
+            w[i] = *reinterpret_cast<const uint32_t *>(&o);
         }
     }
     __device__ __forceinline__ void store(char *out, bool on) const {
@@ -170,11 +178,12 @@ struct LoraPiece {
 // Grid: one cluster per chunk. kMt: m16 tiles of a chunk; kSteps: 32-wide steps of the rank.
 template <int kMt, int kSteps, bool kF32, LoraMode kMode>
 __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
-    constexpr int kRows = 16 * kMt, kSplits = lora_splits(kMt), kParts = kF32 ? 3 : 2, kElement = kF32 ? 4 : 2;
+    constexpr int kRows = 16 * kMt, kSplits = lora_splits(kMt), kParts = lora_parts(kMt, kF32), kElement = kF32 ? 4 : 2;
     extern __shared__ __align__(16) uint8_t s_lora[];
     __shared__ int32_t s_off[kRouteMaxExperts + 2];
-    __shared__ int64_t s_row[kRows];                // row of X, Y and out, -1: none
-    __shared__ int64_t s_y[kRows], s_out[kRows];    // their offsets in Y and out in bytes
+    __shared__ const uint16_t *s_x[kRows];   // the rows' places in X, Y and out, null for none
+    __shared__ const char *s_y[kRows];
+    __shared__ char *s_out[kRows];
     // The first launch of two waits for everything before it and only then lets the second start, so the plan, Y and B are
     // complete for both; the second waits for V.
     if constexpr (kMode != kExpand) griddep_wait();
@@ -193,20 +202,27 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
     for (int i = threadIdx.x; i < kRows; i += kLoraThreads) {
         int64_t m = -1;
         if (i < ch.rows) m = p.row_index ? static_cast<int64_t>(__ldcg(p.row_index + ch.row0 + i)) : ch.row0 + i;
-        s_row[i] = m >= 0 && m < p.M ? m : -1;
-        s_y[i] = m * p.ldy * kElement;
-        s_out[i] = m * p.ldo * kElement;
+        const bool on = m >= 0 && m < p.M;
+        s_x[i] = on ? p.x + m * p.ldx : nullptr;
+        s_y[i] = on ? static_cast<const char *>(p.y) + m * p.ldy * kElement : nullptr;
+        s_out[i] = on ? static_cast<char *>(p.out) + m * p.ldo * kElement : nullptr;
     }
     __syncthreads();
 
     if (ch.a == p.L) {   // rows of no adapter
         if constexpr (kMode == kExpand) griddep_wait();   // out may still be in use
-        const int64_t per = (n_end - n_begin) * 4;
-        for (int64_t i = threadIdx.x; i < ch.rows * per; i += kLoraThreads) {
-            const int64_t m = s_row[i / per], n = n_begin * 32 + i % per * 8;
-            LoraPiece<kF32> y;
-            y.load(static_cast<const char *>(p.y) + (m * p.ldy + n) * kElement, m >= 0 && n < p.N);
-            y.store(static_cast<char *>(p.out) + (m * p.ldo + n) * kElement, m >= 0 && n < p.N);
+        // a warp per row, eight pieces of it in flight
+        constexpr int kAhead = 8;
+        const int64_t stop = min(n_end * 32, p.N);
+        for (int row = warp; row < ch.rows; row += kLoraWarps) {
+            if (s_y[row] == nullptr) continue;
+            for (int64_t n = n_begin * 32 + 8 * lane; n < stop; n += 256 * kAhead) {
+                LoraPiece<kF32> y[kAhead];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) y[k].load(s_y[row] + (n + 256 * k) * kElement, n + 256 * k < stop);
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) y[k].store(s_out[row] + (n + 256 * k) * kElement, n + 256 * k < stop);
+            }
         }
         return;
     }
@@ -224,50 +240,54 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
     }
 
     if constexpr (kMode != kExpand) {
-        // V = X A^T: a warp takes one or two m16 tiles and every kSplits-th k step of the CTA's part
-        constexpr int kMp = kMt == 4 ? 2 : 1;
-        const int m0 = warp % (kMt / kMp) * kMp, split = warp / (kMt / kMp);
-        const uint16_t *x_row[kMp][2];
+        // V = X A^T: a warp takes one m16 tile and every kSplits-th k step of the CTA's part
+        const int mt = warp % kMt, split = warp / kMt;
+        constexpr int kTiles = kSteps == 1 ? 4 : 8;   // n8 tiles of V at a time
+        for (int j0 = 0; j0 < r; j0 += 8 * kTiles) {
+            float acc[kTiles][4] = {};
+            int k = static_cast<int>(k_begin + split) * 32 + 8 * t;   // this lane's first
+            const int k_stop = static_cast<int>(min(k_end * 32, p.K));
+            const uint16_t *a_row[kTiles], *x_row[2];
 #pragma unroll
-        for (int mt = 0; mt < kMp; ++mt)
+            for (int j = 0; j < kTiles; ++j) a_row[j] = j0 + 8 * j < r ? A + (j0 + 8 * j + g) * p.K + k : nullptr;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int64_t m = s_row[16 * (m0 + mt) + 8 * h + g];
-                x_row[mt][h] = m < 0 ? nullptr : p.x + m * p.ldx + 8 * t;
+                const uint16_t *row = s_x[16 * mt + 8 * h + g];
+                x_row[h] = row == nullptr ? nullptr : row + k;
             }
-        constexpr int kTiles = kSteps == 1 ? 4 : 8;   // n8 tiles of V at a time
-        constexpr int kUnroll = kMp == 1 ? 2 : 1;
-        for (int j0 = 0; j0 < r; j0 += 8 * kTiles) {
-            float acc[kMp][kTiles][4] = {};
-#pragma unroll kUnroll
-            for (int64_t s = k_begin + split; s < k_end; s += kSplits) {
-                const int64_t k = s * 32;
-                const bool on = k + 8 * t < p.K;
-                uint4 x[kMp][2], b[kTiles];
+            uint4 x[2];
+            auto load_x = [&](bool on) {
 #pragma unroll
-                for (int mt = 0; mt < kMp; ++mt)
+                for (int h = 0; h < 2; ++h) {
+                    x[h] = lora_ld(x_row[h], on && x_row[h] != nullptr);
+                    if (x_row[h] != nullptr) x_row[h] += 32 * kSplits;
+                }
+            };
+            load_x(k < k_stop);
+#pragma unroll 1
+            for (int s = static_cast<int>(k_begin) + split; s < static_cast<int>(k_end); s += kSplits) {
+                uint4 b[kTiles];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) x[mt][h] = lora_ld(x_row[mt][h] + k, on && x_row[mt][h] != nullptr);
+                for (int j = 0; j < kTiles; ++j) {
+                    b[j] = lora_ld(a_row[j], k < k_stop && a_row[j] != nullptr);
+                    if (a_row[j] != nullptr) a_row[j] += 32 * kSplits;
+                }
+                const uint4 lo = x[0], hi = x[1];
+                k += 32 * kSplits;
+                load_x(k < k_stop);   // the next step's rows of X, from further away than A
 #pragma unroll
-                for (int j = 0; j < kTiles; ++j)
-                    b[j] = lora_ld(A + static_cast<int64_t>(j0 + 8 * j + g) * p.K + k + 8 * t, on && j0 + 8 * j < r);
-#pragma unroll
-                for (int mt = 0; mt < kMp; ++mt)
-#pragma unroll
-                    for (int j = 0; j < kTiles; ++j) {
-                        mma_bf16(acc[mt][j], x[mt][0].x, x[mt][1].x, x[mt][0].y, x[mt][1].y, b[j].x, b[j].y);
-                        mma_bf16(acc[mt][j], x[mt][0].z, x[mt][1].z, x[mt][0].w, x[mt][1].w, b[j].z, b[j].w);
-                    }
+                for (int j = 0; j < kTiles; ++j) {
+                    mma_bf16(acc[j], lo.x, hi.x, lo.y, hi.y, b[j].x, b[j].y);
+                    mma_bf16(acc[j], lo.z, hi.z, lo.w, hi.w, b[j].z, b[j].w);
+                }
             }
 #pragma unroll
-            for (int mt = 0; mt < kMp; ++mt)
-#pragma unroll
-                for (int j = 0; j < kTiles; ++j)
-                    if (j0 + 8 * j < r) {
-                        float *dst = part + (split * kRows + 16 * (m0 + mt) + g) * r + j0 + 8 * j + 2 * t;
-                        *reinterpret_cast<float2 *>(dst) = make_float2(acc[mt][j][0], acc[mt][j][1]);
-                        *reinterpret_cast<float2 *>(dst + 8 * r) = make_float2(acc[mt][j][2], acc[mt][j][3]);
-                    }
+            for (int j = 0; j < kTiles; ++j)
+                if (j0 + 8 * j < r) {
+                    float *dst = part + (split * kRows + 16 * mt + g) * r + j0 + 8 * j + 2 * t;
+                    *reinterpret_cast<float2 *>(dst) = make_float2(acc[j][0], acc[j][1]);
+                    *reinterpret_cast<float2 *>(dst + 8 * r) = make_float2(acc[j][2], acc[j][3]);
+                }
         }
         if constexpr (kMode == kFused)   // the parts' columns past r are zero
             for (int i = threadIdx.x; i < kParts * kRows * (lora_padded_rank(r) - r); i += kLoraThreads) {
@@ -290,7 +310,10 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
     int s = static_cast<int>(n_begin) + warp;
     const uint16_t *b_lane = B + static_cast<int64_t>(n_lane) * r + 8 * t;
     uint8_t *ring = s_lora + (warp * kStages * kPieces * 32 + lane) * 16;   // this lane's piece 0 of stage 0
-    auto b_on = [&](int step, int ks, int i) { return step < s_end && step * 32 + n_lane + 2 * i < N && 32 * ks + 8 * t < r; };
+    uint32_t k_on = 0;   // steps of the rank that this lane has
+#pragma unroll
+    for (int ks = 0; ks < kSteps; ++ks) k_on |= 32 * ks + 8 * t < r ? 1u << ks : 0u;
+    auto b_on = [&](int step, int ks, int i) { return step < s_end && step * 32 + n_lane + 2 * i < N && ((k_on >> ks) & 1); };
     auto b_at = [&](int step, int ks, int i) { return b_lane + (static_cast<int64_t>(step) * 32 + 2 * i) * r + 32 * ks; };
     auto issue = [&](int step, int stage) {
         const uint32_t dst = smem_u32(ring) + stage * kPieces * 512;
@@ -298,8 +321,9 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
 #pragma unroll
             for (int k = 0; k < 2 * kMt; ++k) {
                 const int row = 8 * k + g;
-                if (s_row[row] >= 0 && step * 32 + 8 * t < N) {
-                    const char *src = static_cast<const char *>(p.y) + s_y[row] + (step * 32 + 8 * t) * kElement;
+                const char *src = s_y[row];
+                if (src != nullptr && step * 32 + 8 * t < N) {
+                    src += (step * 32 + 8 * t) * kElement;
 #pragma unroll
                     for (int c = 0; c < kYPieces; ++c) lora_copy16(dst + (k * kYPieces + c) * 512, src + 16 * c, true);
                 }
@@ -394,7 +418,17 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
 #pragma unroll
         for (int mt = 0; mt < kMt; ++mt) {
             if (16 * mt >= ch.rows) break;
-            float acc[4][4] = {};
+            // For bf16 the sums start from Y. For fp32 Y is added last, once: an MMA that adds to it would cut at its last bit
+            // every time.
+            LoraPiece<kF32> y[2];
+            float acc[4][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int c = 0; c < kYPieces; ++c) y[h].v[c] = piece[((2 * mt + h) * kYPieces + c) * 32];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[h].start(i, acc[i][2 * h], acc[i][2 * h + 1]);
+            }
 #pragma unroll
             for (int ks = 0; ks < kSteps; ++ks)
 #pragma unroll
@@ -402,22 +436,16 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
                     const uint16_t *v = v_s + (q * kRows + 16 * mt + g) * vs + 32 * ks + 8 * t;
                     const uint4 lo = *reinterpret_cast<const uint4 *>(v), hi = *reinterpret_cast<const uint4 *>(v + 8 * vs);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        mma_bf16(acc[i], lo.x, hi.x, lo.y, hi.y, b[ks][i].x, b[ks][i].y);
-                        mma_bf16(acc[i], lo.z, hi.z, lo.w, hi.w, b[ks][i].z, b[ks][i].w);
-                    }
+                    for (int i = 0; i < 4; ++i) mma_bf16(acc[i], lo.x, hi.x, lo.y, hi.y, b[ks][i].x, b[ks][i].y);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mma_bf16(acc[i], lo.z, hi.z, lo.w, hi.w, b[ks][i].z, b[ks][i].w);
                 }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                float d[8];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) d[2 * i] = acc[i][2 * h], d[2 * i + 1] = acc[i][2 * h + 1];
-                const int row = 16 * mt + 8 * h + g;
-                LoraPiece<kF32> y;
-#pragma unroll
-                for (int c = 0; c < kYPieces; ++c) y.v[c] = piece[((2 * mt + h) * kYPieces + c) * 32];
-                y.add(d);
-                y.store(static_cast<char *>(p.out) + s_out[row] + (s * 32 + 8 * t) * kElement, s_row[row] >= 0 && s * 32 + 8 * t < N);
+                for (int i = 0; i < 4; ++i) y[h].finish(i, acc[i][2 * h], acc[i][2 * h + 1]);
+                char *dst = s_out[16 * mt + 8 * h + g];
+                y[h].store(dst + (s * 32 + 8 * t) * kElement, dst != nullptr && s * 32 + 8 * t < N);
             }
         }
         if constexpr (kMt > 1) {

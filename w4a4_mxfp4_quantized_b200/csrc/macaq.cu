@@ -1226,7 +1226,7 @@ LoraPlan lora_plan(int64_t M, int32_t L, int32_t r, bool f32) {
     // one chunk per adapter with rows and one for the rows of none, one more per `rows` rows
     p.chunks = std::min<int64_t>(L + 1, M) + M / rows;
     p.two = p.wide && p.chunks > kLoraFusedChunks;
-    p.ws_bytes = p.two ? static_cast<size_t>(p.chunks) * lora_v_bytes(r, 4, f32 ? 3 : 2) : 0;
+    p.ws_bytes = p.two ? static_cast<size_t>(p.chunks) * lora_v_bytes(r, 4, lora_parts(4, f32)) : 0;
     return p;
 }
 
@@ -1248,8 +1248,9 @@ macaq_status run_lora(const LoraArgs &g, const LoraPlan &p, int sms, cudaStream_
     if (p.two) {
         macaq_status s = launch_lora<4, kSteps, kF32, kShrink>(g, p.chunks, kLoraCluster, st);
         if (s != MACAQ_OK) return s;
-        // slices of at least one step per warp, for about four CTAs per SM
-        const int64_t slices = std::max<int64_t>(1, std::min<int64_t>(nsteps / kLoraWarps, (4 * sms + p.chunks - 1) / p.chunks));
+        // slices of at least one step per warp, for one round of two CTAs per SM (what comes before a CTA's first step, about
+        // 5 us, is paid once)
+        const int64_t slices = std::max<int64_t>(1, std::min<int64_t>(nsteps / kLoraWarps, 2 * sms / p.chunks));
         return launch_lora<4, kSteps, kF32, kExpand>(g, p.chunks, static_cast<int>(slices), st);
     }
     // clusters that share a chunk: while SMs are left, and every warp has a step
