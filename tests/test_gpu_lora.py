@@ -98,9 +98,10 @@ def test_column_slices(dtype):
     assert bool(((Y.double() - want).abs() <= bound).all())
 
 
-def test_values_of_other_rows_and_adapters_do_not_leak():
+@pytest.mark.parametrize("M,dtype", [(64, torch.float32), (300, torch.bfloat16), (1500, torch.float32), (1500, torch.bfloat16)])
+def test_values_of_other_rows_and_adapters_do_not_leak(M, dtype):
     """NaN and infinities in one row of X, and in one adapter's A, stay in that row and that adapter's rows."""
-    c = make(3, 64, 256, 256, 16, 4, torch.float32, absent=0.0)
+    c = make(3, M, 256, 256, 24, 4, dtype, absent=0.0)
     c["X"][5] = float("nan")
     c["X"][6, 3] = float("inf")
     c["A"][2, 4] = float("nan")
@@ -124,8 +125,57 @@ def test_bad_plans_stay_inside_the_buffers():
     assert o.intact()
 
 
-def test_captured_graph_and_other_stream_agree():
-    c = make(7, 64, 1024, 768, 16, 9, torch.bfloat16)
+def test_an_infinity_stays_one():
+    """X A^T beyond the parts' range: the output is the infinity that the formula gives, not NaN."""
+    for M, dtype in ((3, torch.bfloat16), (3, torch.float32), (200, torch.bfloat16), (1500, torch.float32)):
+        A = torch.zeros(1, 8, 64, dtype=torch.bfloat16, device="cuda")
+        A[0, :, 0] = 1.0
+        X = torch.zeros(M, 64, dtype=torch.bfloat16, device="cuda")
+        X[1, 0] = float("inf")
+        B = torch.ones(1, 40, 8, dtype=torch.bfloat16, device="cuda")
+        off = torch.tensor([0, M], dtype=torch.int32, device="cuda")
+        out = mq.lora_add(torch.zeros(M, 40, dtype=dtype, device="cuda"), X, A, B, off)
+        torch.cuda.synchronize()
+        assert bool(torch.isinf(out[1]).all()) and bool((out[0] == 0).all()), (M, dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("r", [8, 40, 64, 72, 128])
+def test_many_rows_in_two_launches(r, dtype):
+    """Enough rows for the two-launch form: in place and apart, with its workspace guarded."""
+    c = make(r, 1300, 320, 328, r, 3, dtype)
+    off, row, _ = mq.row_groups(c["ids"], 3)
+    need = mq.lora_workspace_bytes(1300, r, 3, mq.OUT_F32 if dtype == torch.float32 else mq.OUT_BF16)
+    assert need > 0
+    want, bound = reference(c["Y"], c["X"], c["A"], c["B"], c["scale"], off, row)
+    ws, y = Guarded(need), Guarded(c["Y"].numel() * c["Y"].element_size(), dtype=dtype, shape=c["Y"].shape)
+    y.t.copy_(c["Y"])
+    apart = mq.lora_add(c["Y"], c["X"], c["A"], c["B"], off, row, scale=c["scale"], out=torch.empty_like(c["Y"]), workspace=ws.t)
+    mq.lora_add(y.t, c["X"], c["A"], c["B"], off, row, scale=c["scale"], workspace=ws.t)
+    torch.cuda.synchronize()
+    assert ws.intact() and y.intact() and torch.equal(apart, y.t)
+    assert bool(((apart.double() - want).abs() <= bound).all())
+
+
+def test_two_calls_at_once():
+    """The two-launch form on two streams at the same time, each with its own workspace."""
+    cs = [make(s, 1500, 512, 1024, 16, 4, torch.bfloat16) for s in (1, 2)]
+    plans = [mq.row_groups(c["ids"], 4)[:2] for c in cs]
+    alone = [mq.lora_add(c["Y"], c["X"], c["A"], c["B"], *p, out=torch.empty_like(c["Y"])) for c, p in zip(cs, plans)]
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream() for _ in cs], [torch.empty_like(c["Y"]) for c in cs]
+    for _ in range(10):
+        for c, p, s, o in zip(cs, plans, streams, outs):
+            with torch.cuda.stream(s):
+                mq.lora_add(c["Y"], c["X"], c["A"], c["B"], *p, out=o)
+    torch.cuda.synchronize()
+    for a, o in zip(alone, outs):
+        assert torch.equal(a, o)
+
+
+@pytest.mark.parametrize("M", [64, 1500])
+def test_captured_graph_and_other_stream_agree(M):
+    c = make(7, M, 1024, 768, 16, 9, torch.bfloat16)
     off, row, _ = mq.row_groups(c["ids"], 9)
     args = (c["Y"], c["X"], c["A"], c["B"], off, row)
     want = mq.lora_add(*args, scale=c["scale"], out=torch.empty_like(c["Y"]))

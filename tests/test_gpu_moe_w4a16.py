@@ -77,6 +77,12 @@ def test_sizes(T, E, topk, K, I, N):
     check(tokens(T + K, T, K), *routing(E + T, T, E, topk), layer_of(T + E + K, E, K, I, N))
 
 
+@pytest.mark.parametrize("T,E,topk,K,I", [(9, 2, 2, 16384, 128), (9, 3, 1, 128, 16384), (40, 2, 1, 16384, 128), (30, 2, 2, 128, 8192)])
+def test_widest_layers(T, E, topk, K, I):
+    """Panels of so many channels that few rows fit: smaller chunks, and several phases per CTA."""
+    check(tokens(T + K, T, K), *routing(E + T, T, E, topk), layer_of(T + E + K, E, K, I, 256))
+
+
 @pytest.mark.parametrize("b", [1, 16, 32, 64, 128])
 @pytest.mark.parametrize("b_dn", [1, 16, 32, 64, 128])
 def test_hadamard_blocks(b, b_dn):

@@ -60,6 +60,7 @@ def test_lora_add(lib):
     f = caller(lib.macaq_lora_add, Y=P, ldy=256, out=P + 4096, ldo=256, dt=0, X=P, ldx=128, M=4, K=128, N=256, A=P, B=P, r=16, L=3,
                scale=None, off=P, row=P, ws=None, wsb=0, st=None)
     assert f(K=100) == 2 and f(N=100) == 2 and f(r=12) == 2 and f(r=0) == 2 and f(r=136) == 2 and f(L=0) == 2 and f(L=1025) == 2
+    assert f(K=(1 << 24) + 8, ldx=1 << 25) == 2 and f(N=(1 << 24) + 8, ldy=1 << 25, ldo=1 << 25) == 2
     assert f(M=-1) == 2 and f(ldx=120) == 2 and f(ldx=132) == 2 and f(ldy=248) == 2 and f(ldy=260) == 2 and f(ldo=252) == 2
     assert f(out=P, ldo=512) == 2                       # in place with another stride
     assert f(dt=2) == 1

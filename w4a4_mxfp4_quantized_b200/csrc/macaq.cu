@@ -1261,8 +1261,8 @@ macaq_status run_lora(const LoraArgs &g, const LoraPlan &p, int sms, cudaStream_
 }
 
 macaq_status lora_add(const LoraArgs &p, int32_t dtype, void *workspace, size_t ws_bytes, cudaStream_t st) {
-    constexpr int64_t kMax = int64_t(1) << 31;
-    if (p.M < 0 || p.M >= kMax || p.K <= 0 || p.K >= kMax || p.N <= 0 || p.N >= kMax || p.K % 8 || p.N % 8 || p.r < 8 ||
+    constexpr int64_t kMax = int64_t(1) << 31, kWidth = int64_t(1) << 24;   // columns times four bytes stay in 31 bits
+    if (p.M < 0 || p.M >= kMax || p.K <= 0 || p.K > kWidth || p.N <= 0 || p.N > kWidth || p.K % 8 || p.N % 8 || p.r < 8 ||
         p.r > kLoraMaxRank || p.r % 8 || p.L < 1 || p.L > kRouteMaxExperts)
         return MACAQ_ERR_SHAPE;
     if (dtype != MACAQ_OUT_BF16 && dtype != MACAQ_OUT_F32) return MACAQ_ERR_INVALID_ARG;
