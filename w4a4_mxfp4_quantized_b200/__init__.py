@@ -346,7 +346,7 @@ def _cuda(name: str, t: torch.Tensor) -> int:
 
 def _call(fn: str, dev: int, *args) -> None:
     """Calls a library function on the tensors' device (made current for the call) and its current stream."""
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return _call(fn, dev, *args)
     status = getattr(_lib or lib(), fn)(*args, torch._C._cuda_getCurrentRawStream(dev))
@@ -376,14 +376,15 @@ def moe_route(logits: torch.Tensor, topk: int, *, scoring: int = SCORE_SOFTMAX, 
     group_offsets go to act_quant_gather and grouped_linear, pos and weights to moe_combine, all four to moe_w4a16.
     Choices that fall on masked experts are dropped (id -1, weight 0, pos -1)."""
     dev = _cuda("logits", logits)
-    if logits.dim() != 2 or logits.dtype not in _ROWS_DTYPE or (logits.stride(1) != 1 and logits.shape[1] > 1):
+    in_dtype = _ROWS_DTYPE.get(logits.dtype)
+    if logits.dim() != 2 or in_dtype is None:
         raise ValueError("logits: expected a bf16 or fp32 tensor [T, E] with contiguous rows")
     T, E = logits.shape
-    ld = logits.stride(0) if T > 1 else E
+    lp, ld = _rows("logits", logits, logits.dtype, T, E, dev)
     weights = torch.empty(T, topk, dtype=torch.float32, device=dev) if weights is None else weights
     ids = torch.empty(T, topk, dtype=torch.int32, device=dev) if ids is None else ids
     plan, ptrs = _plan_out(T, topk, E, dev, group_offsets, row_index, pos, (T, topk))
-    _call("macaq_moe_route", dev, logits.data_ptr(), _ROWS_DTYPE[logits.dtype], ld, T, E, topk, scoring, int(renormalize),
+    _call("macaq_moe_route", dev, lp, in_dtype, ld, T, E, topk, scoring, int(renormalize),
           scale, _arg("weights", weights, torch.float32, (T, topk), dev), _arg("ids", ids, torch.int32, (T, topk), dev), *ptrs)
     return (weights, ids, *plan)
 
@@ -443,10 +444,13 @@ def lora_workspace_bytes(M: int, r: int, L: int, dtype: int = OUT_BF16) -> int:
 
 def _rows(name: str, t: torch.Tensor, dtype, M: int, N: int, dev):
     """Pointer and row stride of a [M, N] tensor whose rows are contiguous."""
-    if t.dtype is not dtype or t.shape != (M, N) or t.get_device() != dev or (N > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name}: expected a {dtype} tensor of shape {(M, N)} with contiguous rows on cuda:{dev}, got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr(), (t.stride(0) if M > 1 else N)
+    if t.dtype is dtype and t.shape == (M, N) and t.get_device() == dev:
+        if t.is_contiguous():
+            return t.data_ptr(), N
+        if t.stride(1) == 1 or N <= 1:
+            return t.data_ptr(), (t.stride(0) if M > 1 else N)
+    raise ValueError(f"{name}: expected a {dtype} tensor of shape {(M, N)} with contiguous rows on cuda:{dev}, got "
+                     f"{t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def lora_add(Y: torch.Tensor, X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, group_offsets: torch.Tensor,

@@ -289,11 +289,9 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
                     *reinterpret_cast<float2 *>(dst + 8 * r) = make_float2(acc[j][2], acc[j][3]);
                 }
         }
-        if constexpr (kMode == kFused)   // the parts' columns past r are zero
-            for (int i = threadIdx.x; i < kParts * kRows * (lora_padded_rank(r) - r); i += kLoraThreads) {
-                const int per = lora_padded_rank(r) - r;
-                v_s[i / per * vs + r + i % per] = 0;
-            }
+        if constexpr (kMode == kFused)   // the parts are zero where nothing is written: past r, and in rows past the chunk's
+            for (int i = threadIdx.x; i < lora_v_bytes(r, kMt, kParts) / 16; i += kLoraThreads)
+                reinterpret_cast<uint4 *>(v_s)[i] = make_uint4(0u, 0u, 0u, 0u);
         __syncthreads();
         for (int i = threadIdx.x; i < kRows * r; i += kLoraThreads) {
             float v = 0.0f;
@@ -352,22 +350,23 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
         if constexpr (kMt > 1) load_b(s, b);
     }
     if constexpr (kMode != kExpand) {
-        // entries in pairs, an eighth of them per CTA: sum over the cluster, times scale, in bf16 parts to every CTA of the
-        // cluster or to the workspace
+        // Entries in pairs: sum over the cluster, times scale, in bf16 parts. A chunk of 16 rows is small enough for every CTA to
+        // sum all of it for itself; of 64 rows each sums an eighth, for all CTAs of the cluster or for the workspace.
+        constexpr bool kAll = kMt == 1;
         cluster_sync();
         const float scale = p.scale ? __ldg(p.scale + ch.a) : 1.0f;
-        const int pairs = kRows * r / 2;
-        for (int i = rank * pairs / kLoraCluster + threadIdx.x; i < (rank + 1) * pairs / kLoraCluster; i += kLoraThreads) {
-            float v0 = 0.0f, v1 = 0.0f;
+        const int pairs = (kAll ? ch.rows : kRows) * r / 2, at0 = kAll ? 0 : rank * pairs / kLoraCluster,
+                  at1 = kAll ? pairs : (rank + 1) * pairs / kLoraCluster;
+        for (int i = at0 + threadIdx.x; i < at1; i += kLoraThreads) {
+            float a0[kLoraCluster], a1[kLoraCluster], v0 = 0.0f, v1 = 0.0f;
 #pragma unroll
-            for (int c = 0; c < kLoraCluster; ++c) {
-                float a0, a1;
+            for (int c = 0; c < kLoraCluster; ++c)
                 asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
-                             : "=f"(a0), "=f"(a1)
+                             : "=f"(a0[c]), "=f"(a1[c])
                              : "r"(map_to_rank(smem_u32(mine + 2 * i), c))
                              : "memory");
-                v0 += a0, v1 += a1;
-            }
+#pragma unroll
+            for (int c = 0; c < kLoraCluster; ++c) v0 += a0[c], v1 += a1[c];
             v0 *= scale, v1 *= scale;
             const int row = 2 * i / r, col = 2 * i - row * r;
 #pragma unroll
@@ -379,6 +378,8 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
                 const int at = (k * kRows + row) * vs + col;
                 if constexpr (kMode == kShrink) {
                     *reinterpret_cast<uint32_t *>(p.v + static_cast<int64_t>(z) * kParts * kRows * vs + at) = w;
+                } else if constexpr (kAll) {
+                    *reinterpret_cast<uint32_t *>(v_s + at) = w;
                 } else {
 #pragma unroll
                     for (int c = 0; c < kLoraCluster; ++c)
@@ -388,7 +389,12 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
             }
         }
         __syncwarp();
-        cluster_sync();   // V is complete; and no CTA leaves while another reads its sums
+        if constexpr (kAll) {
+            asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // waited for at the end
+            __syncthreads();
+        } else {
+            cluster_sync();   // V is complete; and no CTA leaves while another reads its sums
+        }
         if constexpr (kMode == kShrink) return;
     } else {
         griddep_wait();
@@ -458,6 +464,10 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
                 load_b(s + kLoraWarps, b);
             }
         }
+    }
+    if constexpr (kMode == kFused && kMt == 1) {
+        __syncwarp();
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // no CTA leaves while another reads its sums
     }
 }
 
