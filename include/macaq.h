@@ -310,7 +310,8 @@ macaq_status macaq_moe_w4a16(const void *X, int64_t T, int64_t K, const float *w
  * Low-rank adapters of many requests beside a shared projection:
  *     out[m] = Y[m] + scale[a] * (X[m] A[a]^T) B[a]^T      for the rows m of adapter a
  * with fp32 sums, rounded to out's type. X A^T is held in all of fp32's bits for fp32 outputs; for bf16 outputs in 16
- * bits, and in bf16 for calls of many rows (M > 32 L), which leaves it 2^-9 off: below the output's own rounding.
+ * bits, and in bf16 where the call has many rows (over some 600, and over 32 per adapter), which leaves it 2^-9 off:
+ * below the output's own rounding.
  * Y is the projection's output, from any of the linear calls; X its input (before the activation transform).
  *   Y, out         device [M, N], bf16 or fp32 per dtype (MACAQ_OUT_BF16 / MACAQ_OUT_F32), rows ldy and ldo
  *                  elements apart (>= N): a column slice of a fused projection is fine. out == Y (with

@@ -4,14 +4,14 @@
 //
 // Bound by HBM: for a prefill by Y in and out, for a decode batch by the active adapters' A and B; for a few rows by latency.
 //
-// Few rows (kFused): one launch. A cluster of eight CTAs takes a chunk of up to 16 or 64 rows of one adapter (rows of no
-// adapter are chunks of their own, copied when out is not Y). Each CTA computes the chunk's V = X A^T over an eighth of K;
-// the partial sums are added through distributed shared memory (each CTA adds an eighth of V and sends it to all), and each
-// CTA then adds V B^T to its slice of the columns. With few chunks several clusters share one: each makes V for itself and
-// has a part of the columns. While the first product runs the CTA's part of B is already on its way into L2.
-// Many rows: two launches (kShrink, kExpand), because whole clusters of eight leave SMs idle at the end of a long launch.
-// The first ends with V, in the form the second product takes it, in the workspace; the second takes (chunk, slice of
-// the columns) per CTA without clusters and has its first loads of Y and B under way while the first drains.
+// Few rows (kFused): one launch. A cluster of eight CTAs takes a chunk of up to 16 rows of one adapter (rows of no adapter
+// are chunks of their own, copied when out is not Y). Each CTA computes the chunk's V = X A^T over an eighth of K, sums the
+// cluster's parts of V through distributed shared memory, and adds V B^T to its slice of the columns. With few chunks
+// several clusters share one: each makes V for itself and has a part of the columns. While the first product runs the
+// CTA's part of B is already on its way into L2.
+// Many rows: two launches (kShrink, kExpand) with chunks of 64 rows, because whole clusters of eight leave SMs idle at the
+// end of a long launch. The first ends with V, in the form the second product takes it, in the workspace; the second takes
+// (chunk, slice of the columns) per CTA without clusters and has its first loads of Y and B under way while the first drains.
 //
 // Both products are bf16 MMAs (m16n8k16) fed straight from global memory: lane (g, t) takes 16 bytes, 8 neighbouring k of
 // row g at 8 t of a 32-wide k step, and the two MMAs of the step take their halves; both operands use the same order, so
@@ -35,6 +35,7 @@ constexpr int kLoraWarps = kLoraThreads / 32;
 constexpr int kLoraCluster = 8;
 constexpr int kLoraMaxRank = 128;
 enum LoraMode { kFused, kShrink, kExpand };
+__host__ __device__ constexpr int lora_tiles(LoraMode mode) { return mode == kFused ? 1 : 4; }   // m16 tiles of a chunk
 
 struct LoraArgs {
     const void *y;            // [M, N], rows ldy apart
@@ -175,9 +176,10 @@ struct LoraPiece {
     }
 };
 
-// Grid: one cluster per chunk. kMt: m16 tiles of a chunk; kSteps: 32-wide steps of the rank.
-template <int kMt, int kSteps, bool kF32, LoraMode kMode>
+// Grid: `slices` CTAs per chunk (clusters of eight, without clusters for kExpand). kSteps: 32-wide steps of the rank.
+template <int kSteps, bool kF32, LoraMode kMode>
 __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
+    constexpr int kMt = lora_tiles(kMode);   // m16 tiles of a chunk
     constexpr int kRows = 16 * kMt, kSplits = lora_splits(kMt), kParts = lora_parts(kMt, kF32), kElement = kF32 ? 4 : 2;
     extern __shared__ __align__(16) uint8_t s_lora[];
     __shared__ int32_t s_off[kRouteMaxExperts + 2];
@@ -277,6 +279,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
                 load_x(k < k_stop);   // the next step's rows of X, from further away than A
 #pragma unroll
                 for (int j = 0; j < kTiles; ++j) {
+                    if (kMt == 1 && j0 + 8 * j >= r) break;
                     mma_bf16(acc[j], lo.x, hi.x, lo.y, hi.y, b[j].x, b[j].y);
                     mma_bf16(acc[j], lo.z, hi.z, lo.w, hi.w, b[j].z, b[j].w);
                 }
@@ -293,7 +296,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
             for (int i = threadIdx.x; i < lora_v_bytes(r, kMt, kParts) / 16; i += kLoraThreads)
                 reinterpret_cast<uint4 *>(v_s)[i] = make_uint4(0u, 0u, 0u, 0u);
         __syncthreads();
-        for (int i = threadIdx.x; i < kRows * r; i += kLoraThreads) {
+        for (int i = threadIdx.x; i < (kMt == 1 ? ch.rows : kRows) * r; i += kLoraThreads) {
             float v = 0.0f;
 #pragma unroll
             for (int s = 0; s < kSplits; ++s) v += part[s * kRows * r + i];
@@ -318,6 +321,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
         if (step < s_end) {
 #pragma unroll
             for (int k = 0; k < 2 * kMt; ++k) {
+                if (kMt == 1 && 8 * k >= ch.rows) break;
                 const int row = 8 * k + g;
                 const char *src = s_y[row];
                 if (src != nullptr && step * 32 + 8 * t < N) {
@@ -351,8 +355,8 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
     }
     if constexpr (kMode != kExpand) {
         // Entries in pairs: sum over the cluster, times scale, in bf16 parts. A chunk of 16 rows is small enough for every CTA to
-        // sum all of it for itself; of 64 rows each sums an eighth, for all CTAs of the cluster or for the workspace.
-        constexpr bool kAll = kMt == 1;
+        // sum all of it for itself; of 64 rows each sums an eighth, for the workspace.
+        constexpr bool kAll = kMode == kFused;
         cluster_sync();
         const float scale = p.scale ? __ldg(p.scale + ch.a) : 1.0f;
         const int pairs = (kAll ? ch.rows : kRows) * r / 2, at0 = kAll ? 0 : rank * pairs / kLoraCluster,
@@ -376,16 +380,8 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
                 const float h0 = __uint_as_float(w << 16), h1 = __uint_as_float(w & 0xFFFF0000u);
                 v0 = isinf(h0) ? 0.0f : v0 - h0, v1 = isinf(h1) ? 0.0f : v1 - h1;   // an infinity stays one
                 const int at = (k * kRows + row) * vs + col;
-                if constexpr (kMode == kShrink) {
-                    *reinterpret_cast<uint32_t *>(p.v + static_cast<int64_t>(z) * kParts * kRows * vs + at) = w;
-                } else if constexpr (kAll) {
-                    *reinterpret_cast<uint32_t *>(v_s + at) = w;
-                } else {
-#pragma unroll
-                    for (int c = 0; c < kLoraCluster; ++c)
-                        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to_rank(smem_u32(v_s + at), c)), "r"(w)
-                                     : "memory");
-                }
+                if constexpr (kAll) *reinterpret_cast<uint32_t *>(v_s + at) = w;
+                else *reinterpret_cast<uint32_t *>(p.v + static_cast<int64_t>(z) * kParts * kRows * vs + at) = w;
             }
         }
         __syncwarp();
@@ -393,7 +389,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
             asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // waited for at the end
             __syncthreads();
         } else {
-            cluster_sync();   // V is complete; and no CTA leaves while another reads its sums
+            cluster_sync();   // no CTA leaves while another reads its sums
         }
         if constexpr (kMode == kShrink) return;
     } else {
@@ -427,9 +423,10 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
             // For bf16 the sums start from Y. For fp32 Y is added last, once: an MMA that adds to it would cut at its last bit
             // every time.
             LoraPiece<kF32> y[2];
-            float acc[4][4];
+            float acc[4][4] = {};
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
+                if (kMt == 1 && h == 1 && ch.rows <= 8) break;   // rows 8 .. 15: none (their sums are not looked at)
 #pragma unroll
                 for (int c = 0; c < kYPieces; ++c) y[h].v[c] = piece[((2 * mt + h) * kYPieces + c) * 32];
 #pragma unroll
@@ -448,6 +445,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
                 }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
+                if (kMt == 1 && h == 1 && ch.rows <= 8) break;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) y[h].finish(i, acc[i][2 * h], acc[i][2 * h + 1]);
                 char *dst = s_out[16 * mt + 8 * h + g];
@@ -465,7 +463,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
             }
         }
     }
-    if constexpr (kMode == kFused && kMt == 1) {
+    if constexpr (kMode == kFused) {
         __syncwarp();
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // no CTA leaves while another reads its sums
     }

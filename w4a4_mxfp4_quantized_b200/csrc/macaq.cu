@@ -1209,34 +1209,35 @@ macaq_status moe_w4a16(const MoeArgs &a, void *workspace, size_t ws_bytes, cudaS
 }
 
 // ------------------------------------------------------------------------ low-rank adapters
-constexpr int64_t kLoraFusedChunks = 16;   // wide chunks that one launch takes
+constexpr int64_t kLoraNarrowChunks = 37;   // 16-row chunks up to which no others are used
 
-// How a call is cut: 64-row chunks once adapters have some (A and B are read per chunk); two launches once the chunks alone
-// fill the GPU.
+// How a call is cut. 16-row chunks while one round of clusters takes them all (37 of eight CTAs, two per SM): 400 rows of 4
+// adapters, rank 64, 4096 -> 14336, take 24 us against 28 us in 64-row chunks. Beyond, 64-row chunks where adapters have more
+// than 32 rows, since A and B are read per chunk: 700 rows of 8 adapters, rank 32, 26 against 32 us; 2048 of 40, rank 16, 55
+// against 68 us. Those take two launches: 33.6 against 45.2 us in one for 1000 rows of 4 adapters, rank 64.
 struct LoraPlan {
-    bool wide, two;
+    bool wide;
     int64_t chunks;
     size_t ws_bytes;
 };
 
 LoraPlan lora_plan(int64_t M, int32_t L, int32_t r, bool f32) {
     LoraPlan p;
-    p.wide = M > 32 * static_cast<int64_t>(L);
+    p.wide = std::min<int64_t>(L + 1, M) + M / 16 > kLoraNarrowChunks && M > 32 * static_cast<int64_t>(L);
     const int rows = p.wide ? 64 : 16;
     // one chunk per adapter with rows and one for the rows of none, one more per `rows` rows
     p.chunks = std::min<int64_t>(L + 1, M) + M / rows;
-    p.two = p.wide && p.chunks > kLoraFusedChunks;
-    p.ws_bytes = p.two ? static_cast<size_t>(p.chunks) * lora_v_bytes(r, 4, lora_parts(4, f32)) : 0;
+    p.ws_bytes = p.wide ? static_cast<size_t>(p.chunks) * lora_v_bytes(r, 4, lora_parts(4, f32)) : 0;
     return p;
 }
 
-template <int kMt, int kSteps, bool kF32, LoraMode kMode>
-macaq_status launch_lora(LoraArgs g, int64_t chunks, int slices, cudaStream_t st) {
-    auto k = lora_add_kernel<kMt, kSteps, kF32, kMode>;
-    const size_t smem = lora_smem_bytes(g.r, kMt, kSteps, kF32, kMode);
+template <int kSteps, bool kF32, LoraMode kMode>
+macaq_status launch_lora(LoraArgs g, int64_t chunks, int64_t slices, cudaStream_t st) {
+    auto k = lora_add_kernel<kSteps, kF32, kMode>;
+    const size_t smem = lora_smem_bytes(g.r, lora_tiles(kMode), kSteps, kF32, kMode);
     macaq_status s = set_smem(k, smem);
     if (s != MACAQ_OK) return s;
-    g.slices = slices;
+    g.slices = static_cast<int32_t>(slices);
     if (chunks * slices >= (int64_t(1) << 31)) return MACAQ_ERR_SHAPE;
     return launch(k, dim3(static_cast<unsigned>(chunks * slices)), dim3(kLoraThreads), smem, st,
                   kMode == kExpand ? 1 : kLoraCluster, g);
@@ -1245,19 +1246,17 @@ macaq_status launch_lora(LoraArgs g, int64_t chunks, int slices, cudaStream_t st
 template <int kSteps, bool kF32>
 macaq_status run_lora(const LoraArgs &g, const LoraPlan &p, int sms, cudaStream_t st) {
     const int64_t nsteps = (g.N + 31) / 32;
-    if (p.two) {
-        macaq_status s = launch_lora<4, kSteps, kF32, kShrink>(g, p.chunks, kLoraCluster, st);
+    if (p.wide) {
+        const macaq_status s = launch_lora<kSteps, kF32, kShrink>(g, p.chunks, kLoraCluster, st);
         if (s != MACAQ_OK) return s;
         // slices of at least one step per warp, for one round of two CTAs per SM (what comes before a CTA's first step, about
         // 5 us, is paid once)
         const int64_t slices = std::max<int64_t>(1, std::min<int64_t>(nsteps / kLoraWarps, 2 * sms / p.chunks));
-        return launch_lora<4, kSteps, kF32, kExpand>(g, p.chunks, static_cast<int>(slices), st);
+        return launch_lora<kSteps, kF32, kExpand>(g, p.chunks, slices, st);
     }
     // clusters that share a chunk: while SMs are left, and every warp has a step
     const int64_t share = std::max<int64_t>(1, std::min<int64_t>(2 * sms / (kLoraCluster * p.chunks), nsteps / (kLoraCluster * kLoraWarps)));
-    const int slices = static_cast<int>(share) * kLoraCluster;
-    return p.wide ? launch_lora<4, kSteps, kF32, kFused>(g, p.chunks, slices, st)
-                  : launch_lora<1, kSteps, kF32, kFused>(g, p.chunks, slices, st);
+    return launch_lora<kSteps, kF32, kFused>(g, p.chunks, share * kLoraCluster, st);
 }
 
 macaq_status lora_add(const LoraArgs &p, int32_t dtype, void *workspace, size_t ws_bytes, cudaStream_t st) {
