@@ -1044,7 +1044,7 @@ bool plan_shape_ok(int64_t T, int32_t topk, int32_t E) {
 // The row sort; kVpl > 0: with the choice of experts before it.
 template <int kVpl>
 macaq_status run_row_groups(const RouteArgs &t, const GroupArgs &g, cudaStream_t st) {
-    const size_t smem = (kGroupWarps + 2) * static_cast<size_t>(g.E + 1) * sizeof(int32_t);
+    const size_t smem = (kGroupWarps + 3) * static_cast<size_t>(g.E + 1) * sizeof(int32_t);
     macaq_status s = set_smem(row_groups_kernel<kVpl>, smem);
     if (s != MACAQ_OK) return s;
     const bool wide = g.R > kGroupWide;   // 16 CTAs: beyond the portable cluster size, hence allowed explicitly
