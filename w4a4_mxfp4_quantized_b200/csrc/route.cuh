@@ -223,6 +223,8 @@ __global__ void __launch_bounds__(kGroupThreads) row_groups_kernel(RouteArgs t, 
         first[b] = lower;
         sums[b] = all;
     }
+    __syncwarp();
+    if (ctas > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // done with the others' totals
     __syncthreads();
     const int b = threadIdx.x;
     const int32_t total = b < a.E ? sums[b] : 0;
@@ -275,7 +277,8 @@ __global__ void __launch_bounds__(kGroupThreads) row_groups_kernel(RouteArgs t, 
             }
         }
     }
-    if (ctas > 1) cluster_sync();   // no CTA leaves while another reads its totals
+    __syncwarp();
+    if (ctas > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // no CTA leaves while its totals are read
 }
 
 }  // namespace macaq
