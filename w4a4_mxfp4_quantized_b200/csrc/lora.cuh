@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
         }
         cp_async_commit();   // an empty group keeps groups and steps in step
     };
-    uint4 b[kSteps][4], b_next[kSteps][4];   // kMt > 1: B in registers, the next step's on its way while one is multiplied
+    uint4 b[kSteps][4];   // a second set for the next step's, loaded ahead, cost registers and time (50.7 against 45.7 us)
     auto load_b = [&](int step, uint4 (&to)[kSteps][4]) {
 #pragma unroll
         for (int ks = 0; ks < kSteps; ++ks)
@@ -409,7 +409,6 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
 #pragma unroll 1
     for (; s < s_end; s += kLoraWarps) {
         issue(s + (kStages - 1) * kLoraWarps, stage == 0 ? kStages - 1 : stage - 1);
-        if constexpr (kMt > 1 && kSteps < 4) load_b(s + kLoraWarps, b_next);
         cp_async_wait<kStages - 1>();   // this lane's copies of the step have landed
         const uint4 *piece = reinterpret_cast<const uint4 *>(ring + stage * kPieces * 512);
         stage = stage == kStages - 1 ? 0 : stage + 1;
@@ -452,16 +451,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
                 y[h].store(dst + (s * 32 + 8 * t) * kElement, dst != nullptr && s * 32 + 8 * t < N);
             }
         }
-        if constexpr (kMt > 1) {
-            if constexpr (kSteps < 4) {
-#pragma unroll
-                for (int ks = 0; ks < kSteps; ++ks)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) b[ks][i] = b_next[ks][i];
-            } else {
-                load_b(s + kLoraWarps, b);
-            }
-        }
+        if constexpr (kMt > 1) load_b(s + kLoraWarps, b);
     }
     if constexpr (kMode == kFused) {
         __syncwarp();
