@@ -28,6 +28,11 @@
 // without looking at them; otherwise 1/s joins the weights' scale of the group. fp16's 11 bits round x' and h' 8 times
 // finer than the output's bf16.
 //
+// Measured on B200 (128 experts, top-8, 2048 x 768; a graph that cycles three layers): one token 16.0 us (20.2 MB), 8 tokens
+// 35.5 us (130 MB), 64 tokens 72.2 us (318 MB, 4.4 TB/s). With 64 tokens the two weight streams themselves run at 5.9 and
+// 5.8 TB/s (36 and 18 us) of the 6.5 that a copy reaches; the rest is three starts (plan 1.3 us, first loads and panel 3 to
+// 5 us, a launch's end to the next one's first instruction 1 to 1.5 us) and the closing of cut items (1 us). One token
+// is made of those latencies alone.
 // Sources: glonce.com page on MACaQ, paragraph 3 (weight-only serving) and paragraph 5 (grouped matmul);
 // aipolix.com page, paragraph 2 (the transform at the input of every linear).
 #pragma once

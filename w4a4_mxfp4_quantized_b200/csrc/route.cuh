@@ -14,8 +14,10 @@
 // (entry / topk) of sorted row r; entries of no group follow the last group in their order.
 //
 // Bound by latency: a prefill's 65,536 entries are 0.8 MB. One CTA sorts up to 2,048 entries, a cluster of eight CTAs more
-// (their counts meet in distributed shared memory, so one launch and no workspace do); with up to 512 tokens the
+// (their counts meet in distributed shared memory, so one launch and no workspace do); with up to 256 tokens the
 // same launch chooses the experts too, a warp per token.
+// Measured on B200 (128 experts, top-8): one token 4.9 us, 64 tokens 6.1, 8192 tokens 15.5 us in two launches (5.5 for the
+// choice, 9.6 for the sort); the sort of 64 entries 3.4 us.
 #pragma once
 
 #include <stdint.h>
