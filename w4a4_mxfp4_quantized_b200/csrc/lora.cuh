@@ -10,18 +10,21 @@
 // several clusters share one: each makes V for itself and has a part of the columns. While the first product runs the
 // CTA's part of B is already on its way into L2.
 // Many rows: two launches (kShrink, kExpand) with chunks of 64 rows, because whole clusters of eight leave SMs idle at the
-// end of a long launch. The first ends with V, in the form the second product takes it, in the workspace; the second takes
+// end of a long launch. The first still has a cluster of eight per chunk, each CTA with an eighth of K: tiles of X and A come
+// through a ring in shared memory, most of a CTA's part at once (4096 wide: 8 tiles, 6 in flight), so that a
+// launch of a few microseconds waits for memory once. It ends with V, in the form the second product takes it, in the
+// workspace (loads straight to the MMAs, a step ahead, took 45.8 us in all for the 2048 rows below). The second takes
 // (chunk, slice of the columns) per CTA without clusters and has its first loads of Y and B under way while the first drains.
 //
-// Both products are bf16 MMAs (m16n8k16) fed straight from global memory: lane (g, t) takes 16 bytes, 8 neighbouring k of
+// The other products are bf16 MMAs (m16n8k16) fed straight from global memory: lane (g, t) takes 16 bytes, 8 neighbouring k of
 // row g at 8 t of a 32-wide k step, and the two MMAs of the step take their halves; both operands use the same order, so
 // the sum over k is complete. In the second product the 32 columns of a step are dealt to the four n8 tiles so that a lane
 // ends up with 8 neighbouring columns of a row: Y moves in 16-byte pieces, through a ring of cp.async stages in which each
 // lane reads back what it copied itself (no barrier; the copies of the next steps are in flight while one is added). V is held in
 // up to three bf16 parts (8, 16 or 24 bits).
 // Measured on B200 (4096 -> 14336, a graph that cycles three batches): one row of rank 16 5.4 us; 64 rows over 32 adapters of
-// rank 16 12.4 us (19.7 MB; find 1.0, V 1.9, cluster sum 2.0, columns 5 us); 2048 rows of 4 adapters of rank 64 45.8 us
-// (142 MB, 3.1 TB/s: 14 us for V, most of it starts and the cluster's sum, and 27 us for the columns, whose warps
+// rank 16 12.4 us (19.7 MB; find 1.0, V 1.9, cluster sum 2.0, columns 5 us); 2048 rows of 4 adapters of rank 64 40.9 us
+// (142 MB, 3.5 TB/s: 10 us for V, most of it starts and the cluster's sum, and 27 us for the columns, whose warps
 // wait on one another's MMAs, shared memory and stores rather than on HBM).
 #pragma once
 
@@ -38,6 +41,7 @@ constexpr int kLoraThreads = 256;
 constexpr int kLoraWarps = kLoraThreads / 32;
 constexpr int kLoraCluster = 8;
 constexpr int kLoraMaxRank = 128;
+constexpr int kLoraShrinkBytes = 96 * 1024;
 enum LoraMode { kFused, kShrink, kExpand };
 __host__ __device__ constexpr int lora_tiles(LoraMode mode) { return mode == kFused ? 1 : 4; }   // m16 tiles of a chunk
 
@@ -62,7 +66,6 @@ __host__ __device__ constexpr int lora_padded_rank(int r) { return r <= 32 ? 32 
 __host__ __device__ constexpr int lora_v_stride(int r) {   // bf16; 64 bytes off a multiple of 128: no bank conflicts
     return lora_padded_rank(r) == 32 ? 32 : lora_padded_rank(r) + 32;
 }
-__host__ __device__ constexpr int lora_splits(int mt) { return kLoraWarps / mt; }
 // bf16 parts that V is held in: three for fp32 outputs; for bf16 outputs two, and one for chunks of 64 rows, where the
 // second costs a quarter of the launch (2048 rows of rank 64 on 14336 columns: 38 against 29 us) and V's rounding, 2^-9 of
 // the adapter's share, stays under the output's own.
@@ -76,16 +79,21 @@ __host__ __device__ constexpr int lora_ring_stages(int mt, int steps, bool f32) 
 __host__ __device__ constexpr int lora_ring_bytes(int mt, int steps, bool f32) {
     return kLoraWarps * lora_ring_stages(mt, steps, f32) * lora_ring_pieces(mt, steps, f32) * 512;
 }
-// Offsets: [ring, over the partial sums][the CTA's sum][parts of V]
-__host__ __device__ constexpr int lora_sum_offset(int r, int mt, int steps, bool f32, LoraMode mode) {
-    const int part = mode == kExpand ? 0 : lora_splits(mt) * 16 * mt * r * 4, ring = mode == kShrink ? 0 : lora_ring_bytes(mt, steps, f32);
+// kShrink: tiles of 64 k of the chunk's 64 rows of X and of A's rows, two CTAs' stages to an SM.
+__host__ __device__ constexpr int lora_shrink_stage(int steps) { return (64 + 32 * steps) * 128; }
+__host__ __device__ constexpr int lora_shrink_stages(int steps) { return kLoraShrinkBytes / lora_shrink_stage(steps); }
+// Offsets, kFused: [ring, over the partial sums][the CTA's sum][parts of V]; kExpand: [ring][parts of V]; kShrink: [ring, under
+// the CTA's sum in the end]
+__host__ __device__ constexpr int lora_sum_offset(int r, int steps, bool f32) {
+    const int part = kLoraWarps * 16 * r * 4, ring = lora_ring_bytes(1, steps, f32);
     return part > ring ? part : ring;
 }
-__host__ __device__ constexpr int lora_v_offset(int r, int mt, int steps, bool f32, LoraMode mode) {
-    return lora_sum_offset(r, mt, steps, f32, mode) + (mode == kExpand ? 0 : 16 * mt * r * 4);
+__host__ __device__ constexpr int lora_v_offset(int r, int steps, bool f32, LoraMode mode) {
+    return mode == kFused ? lora_sum_offset(r, steps, f32) + 16 * r * 4 : lora_ring_bytes(4, steps, f32);
 }
-__host__ __device__ constexpr int lora_smem_bytes(int r, int mt, int steps, bool f32, LoraMode mode) {
-    return lora_v_offset(r, mt, steps, f32, mode) + (mode == kShrink ? 0 : lora_v_bytes(r, mt, lora_parts(mt, f32)));
+__host__ __device__ constexpr int lora_smem_bytes(int r, int steps, bool f32, LoraMode mode) {
+    if (mode == kShrink) return lora_shrink_stages(steps) * lora_shrink_stage(steps);
+    return lora_v_offset(r, steps, f32, mode) + lora_v_bytes(r, lora_tiles(mode), lora_parts(lora_tiles(mode), f32));
 }
 
 __device__ __forceinline__ void lora_copy16(uint32_t dst, const void *src, bool on) {   // off: zeros
@@ -184,7 +192,7 @@ struct LoraPiece {
 template <int kSteps, bool kF32, LoraMode kMode>
 __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
     constexpr int kMt = lora_tiles(kMode);   // m16 tiles of a chunk
-    constexpr int kRows = 16 * kMt, kSplits = lora_splits(kMt), kParts = lora_parts(kMt, kF32), kElement = kF32 ? 4 : 2;
+    constexpr int kRows = 16 * kMt, kParts = lora_parts(kMt, kF32), kElement = kF32 ? 4 : 2;
     extern __shared__ __align__(16) uint8_t s_lora[];
     __shared__ int32_t s_off[kRouteMaxExperts + 2];
     __shared__ const uint16_t *s_x[kRows];   // the rows' places in X, Y and out, null for none
@@ -202,9 +210,10 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
         return;
     }
     const int r = p.r;
-    // this CTA's columns, in steps of 32, and k steps of 32
+    // this CTA's columns, in steps of 32, and k, in steps of 32 or 64
     const int64_t nsteps = (p.N + 31) / 32, n_begin = nsteps * slice / p.slices, n_end = nsteps * (slice + 1) / p.slices;
-    const int64_t ksteps = (p.K + 31) / 32, k_begin = ksteps * rank / kLoraCluster, k_end = ksteps * (rank + 1) / kLoraCluster;
+    constexpr int kWide = kMode == kShrink ? 64 : 32;
+    const int64_t ksteps = (p.K + kWide - 1) / kWide, k_begin = ksteps * rank / kLoraCluster, k_end = ksteps * (rank + 1) / kLoraCluster;
     for (int i = threadIdx.x; i < kRows; i += kLoraThreads) {
         int64_t m = -1;
         if (i < ch.rows) m = p.row_index ? static_cast<int64_t>(__ldcg(p.row_index + ch.row0 + i)) : ch.row0 + i;
@@ -235,9 +244,9 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
 
     const uint16_t *A = p.A + static_cast<int64_t>(ch.a) * r * p.K, *B = p.B + static_cast<int64_t>(ch.a) * p.N * r;
     float *part = reinterpret_cast<float *>(s_lora);                                                   // [split][row][r]
-    float *mine = reinterpret_cast<float *>(s_lora + lora_sum_offset(r, kMt, kSteps, kF32, kMode));     // [row][r]
+    float *mine = reinterpret_cast<float *>(s_lora + (kMode == kFused ? lora_sum_offset(r, kSteps, kF32) : 0));  // [row][r]
     const int vs = lora_v_stride(r);
-    uint16_t *v_s = reinterpret_cast<uint16_t *>(s_lora + lora_v_offset(r, kMt, kSteps, kF32, kMode));  // [part][row][vs]
+    uint16_t *v_s = reinterpret_cast<uint16_t *>(s_lora + lora_v_offset(r, kSteps, kF32, kMode));      // [part][row][vs]
     if constexpr (kMode == kFused) {   // this CTA's part of B, towards L2
         const char *from = reinterpret_cast<const char *>(B + n_begin * 32 * r);
         const int64_t bytes = (min(n_end * 32, p.N) - n_begin * 32) * r * 2;
@@ -245,20 +254,19 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
             asm volatile("prefetch.global.L2 [%0];" ::"l"(from + i));
     }
 
-    if constexpr (kMode != kExpand) {
-        // V = X A^T: a warp takes one m16 tile and every kSplits-th k step of the CTA's part
-        const int mt = warp % kMt, split = warp / kMt;
+    if constexpr (kMode == kFused) {
+        // V = X A^T: a warp takes every eighth k step of the CTA's part
         constexpr int kTiles = kSteps == 1 ? 4 : 8;   // n8 tiles of V at a time
         for (int j0 = 0; j0 < r; j0 += 8 * kTiles) {
             float acc[kTiles][4] = {};
-            int k = static_cast<int>(k_begin + split) * 32 + 8 * t;   // this lane's first
+            int k = static_cast<int>(k_begin + warp) * 32 + 8 * t;   // this lane's first
             const int k_stop = static_cast<int>(min(k_end * 32, p.K));
             const uint16_t *a_row[kTiles], *x_row[2];
 #pragma unroll
             for (int j = 0; j < kTiles; ++j) a_row[j] = j0 + 8 * j < r ? A + (j0 + 8 * j + g) * p.K + k : nullptr;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint16_t *row = s_x[16 * mt + 8 * h + g];
+                const uint16_t *row = s_x[8 * h + g];
                 x_row[h] = row == nullptr ? nullptr : row + k;
             }
             uint4 x[2];
@@ -266,24 +274,24 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     x[h] = lora_ld(x_row[h], on && x_row[h] != nullptr);
-                    if (x_row[h] != nullptr) x_row[h] += 32 * kSplits;
+                    if (x_row[h] != nullptr) x_row[h] += 32 * kLoraWarps;
                 }
             };
             load_x(k < k_stop);
 #pragma unroll 1
-            for (int s = static_cast<int>(k_begin) + split; s < static_cast<int>(k_end); s += kSplits) {
+            for (int s = static_cast<int>(k_begin) + warp; s < static_cast<int>(k_end); s += kLoraWarps) {
                 uint4 b[kTiles];
 #pragma unroll
                 for (int j = 0; j < kTiles; ++j) {
                     b[j] = lora_ld(a_row[j], k < k_stop && a_row[j] != nullptr);
-                    if (a_row[j] != nullptr) a_row[j] += 32 * kSplits;
+                    if (a_row[j] != nullptr) a_row[j] += 32 * kLoraWarps;
                 }
                 const uint4 lo = x[0], hi = x[1];
-                k += 32 * kSplits;
+                k += 32 * kLoraWarps;
                 load_x(k < k_stop);   // the next step's rows of X, from further away than A
 #pragma unroll
                 for (int j = 0; j < kTiles; ++j) {
-                    if (kMt == 1 && j0 + 8 * j >= r) break;
+                    if (j0 + 8 * j >= r) break;
                     mma_bf16(acc[j], lo.x, hi.x, lo.y, hi.y, b[j].x, b[j].y);
                     mma_bf16(acc[j], lo.z, hi.z, lo.w, hi.w, b[j].z, b[j].w);
                 }
@@ -291,21 +299,83 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
 #pragma unroll
             for (int j = 0; j < kTiles; ++j)
                 if (j0 + 8 * j < r) {
-                    float *dst = part + (split * kRows + 16 * mt + g) * r + j0 + 8 * j + 2 * t;
+                    float *dst = part + (warp * kRows + g) * r + j0 + 8 * j + 2 * t;
                     *reinterpret_cast<float2 *>(dst) = make_float2(acc[j][0], acc[j][1]);
                     *reinterpret_cast<float2 *>(dst + 8 * r) = make_float2(acc[j][2], acc[j][3]);
                 }
         }
-        if constexpr (kMode == kFused)   // the parts are zero where nothing is written: past r, and in rows past the chunk's
-            for (int i = threadIdx.x; i < lora_v_bytes(r, kMt, kParts) / 16; i += kLoraThreads)
-                reinterpret_cast<uint4 *>(v_s)[i] = make_uint4(0u, 0u, 0u, 0u);
+        // the parts of V are zero where nothing is written: past r, and in rows past the chunk's
+        for (int i = threadIdx.x; i < lora_v_bytes(r, kMt, kParts) / 16; i += kLoraThreads)
+            reinterpret_cast<uint4 *>(v_s)[i] = make_uint4(0u, 0u, 0u, 0u);
         __syncthreads();
-        for (int i = threadIdx.x; i < (kMt == 1 ? ch.rows : kRows) * r; i += kLoraThreads) {
+        for (int i = threadIdx.x; i < ch.rows * r; i += kLoraThreads) {
             float v = 0.0f;
 #pragma unroll
-            for (int s = 0; s < kSplits; ++s) v += part[s * kRows * r + i];
+            for (int s = 0; s < kLoraWarps; ++s) v += part[s * kRows * r + i];
             mine[i] = v;
         }
+    }
+    if constexpr (kMode == kShrink) {
+        // V = X A^T: tiles of 64 k of both operands through a ring in shared memory, rows of 128 bytes whose 16-byte pieces are
+        // exchanged by row % 8. A warp has one m16 tile of the rows and half of the rank.
+        constexpr int kStages = lora_shrink_stages(kSteps), kStage = lora_shrink_stage(kSteps), kTiles = 2 * kSteps;
+        const uint32_t ring = smem_u32(s_lora);
+        const int piece = threadIdx.x & 7, row = threadIdx.x >> 3;   // this thread copies this piece of every 32nd row
+        const uint16_t *x_row[2] = {s_x[row], s_x[row + 32]}, *a_row = A + static_cast<int64_t>(row) * p.K;
+        const int64_t a_step = 32 * p.K;
+        auto issue = [&](int64_t step, int stage) {
+            if (step < k_end) {
+                const int64_t k = step * 64 + 8 * piece;
+                const bool in = k < p.K;
+                const uint32_t dst = ring + stage * kStage + row * 128 + ((piece ^ (row & 7)) << 4);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const bool on = in && x_row[i] != nullptr;
+                    lora_copy16(dst + i * 4096, on ? x_row[i] + k : p.x, on);
+                }
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    const bool on = in && row + 32 * i < r;
+                    lora_copy16(dst + 8192 + i * 4096, on ? a_row + i * a_step + k : A, on);
+                }
+            }
+            cp_async_commit();   // an empty group keeps groups and stages in step
+        };
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) issue(k_begin + i, i);
+        const int mt = warp % 4, tile0 = warp / 4 * kTiles;
+        const uint32_t x_at = ring + (16 * mt + (lane & 15)) * 128, a_at = ring + 8192 + (8 * tile0 + 8 * (lane >> 4) + (lane & 7)) * 128;
+        float acc[kTiles][4] = {};
+        int stage = 0;
+#pragma unroll 1
+        for (int64_t step = k_begin; step < k_end; ++step) {
+            cp_async_wait<kStages - 2>();
+            __syncthreads();   // the step's tiles are complete, and nobody reads those of the step before
+            issue(step + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
+            if (16 * mt < ch.rows) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t x[4];
+                    ldmatrix_x4(x, x_at + stage * kStage + (((2 * c + (lane >> 4)) ^ (lane & 7)) << 4));
+#pragma unroll
+                    for (int j = 0; j < kTiles; j += 2) {
+                        uint32_t b[4];
+                        ldmatrix_x4(b, a_at + stage * kStage + j * 1024 + (((2 * c + ((lane >> 3) & 1)) ^ (lane & 7)) << 4));
+                        mma_bf16(acc[j], x[0], x[1], x[2], x[3], b[0], b[1]);
+                        mma_bf16(acc[j + 1], x[0], x[1], x[2], x[3], b[2], b[3]);
+                    }
+                }
+            }
+            stage = stage == kStages - 1 ? 0 : stage + 1;
+        }
+        __syncthreads();   // the sums lie over the ring
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j)
+            if (8 * (tile0 + j) < r) {
+                float *dst = mine + (16 * mt + g) * r + 8 * (tile0 + j) + 2 * t;
+                *reinterpret_cast<float2 *>(dst) = make_float2(acc[j][0], acc[j][1]);
+                *reinterpret_cast<float2 *>(dst + 8 * r) = make_float2(acc[j][2], acc[j][3]);
+            }
     }
     // The second product's loads. A warp takes every eighth 32-column step; the first copies set out here, before V is complete.
     // Logical column c of n8 tile i is column 8 (c / 2) + 2 i + c % 2 of the step.

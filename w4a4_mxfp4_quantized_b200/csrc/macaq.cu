@@ -1234,7 +1234,7 @@ LoraPlan lora_plan(int64_t M, int32_t L, int32_t r, bool f32) {
 template <int kSteps, bool kF32, LoraMode kMode>
 macaq_status launch_lora(LoraArgs g, int64_t chunks, int64_t slices, cudaStream_t st) {
     auto k = lora_add_kernel<kSteps, kF32, kMode>;
-    const size_t smem = lora_smem_bytes(g.r, lora_tiles(kMode), kSteps, kF32, kMode);
+    const size_t smem = lora_smem_bytes(g.r, kSteps, kF32, kMode);
     macaq_status s = set_smem(k, smem);
     if (s != MACAQ_OK) return s;
     g.slices = static_cast<int32_t>(slices);
