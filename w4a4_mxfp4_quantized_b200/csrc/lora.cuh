@@ -10,7 +10,7 @@
 // several clusters share one: each makes V for itself and has a part of the columns. While the first product runs the
 // CTA's part of B is already on its way into L2.
 // Many rows: two launches (kShrink, kExpand) with chunks of 64 rows, because whole clusters of eight leave SMs idle at the
-// end of a long launch. The first still has a cluster of eight per chunk, each CTA with an eighth of K: tiles of X and A come
+// end of a long launch. The first still has a cluster per chunk, each CTA with its share of K: tiles of X and A come
 // through a ring in shared memory, most of a CTA's part at once (4096 wide: 8 tiles, 6 in flight), so that a
 // launch of a few microseconds waits for memory once. It ends with V, in the form the second product takes it, in the
 // workspace (loads straight to the MMAs, a step ahead, took 45.8 us in all for the 2048 rows below). The second takes
@@ -188,7 +188,7 @@ struct LoraPiece {
     }
 };
 
-// Grid: `slices` CTAs per chunk (clusters of eight, without clusters for kExpand). kSteps: 32-wide steps of the rank.
+// Grid: `slices` CTAs per chunk: clusters of eight (kFused), one cluster of 1 to 8 (kShrink), without clusters (kExpand). kSteps: 32-wide steps of the rank.
 template <int kSteps, bool kF32, LoraMode kMode>
 __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
     constexpr int kMt = lora_tiles(kMode);   // m16 tiles of a chunk
@@ -203,7 +203,8 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
     if constexpr (kMode != kExpand) griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int rank = blockIdx.x % kLoraCluster, z = blockIdx.x / p.slices, slice = blockIdx.x % p.slices;
+    const int cluster = kMode == kShrink ? p.slices : kLoraCluster, log2_cluster = 31 - __clz(cluster);   // a power of two
+    const int rank = blockIdx.x & (cluster - 1), z = blockIdx.x / p.slices, slice = blockIdx.x % p.slices;
     const LoraChunk ch = lora_find_chunk(p, z, kRows, s_off);
     if (ch.rows == 0 || (ch.a == p.L && (kMode == kShrink || p.out == p.y))) {   // the same for the whole cluster
         if constexpr (kMode == kExpand) griddep_wait();
@@ -213,7 +214,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
     // this CTA's columns, in steps of 32, and k, in steps of 32 or 64
     const int64_t nsteps = (p.N + 31) / 32, n_begin = nsteps * slice / p.slices, n_end = nsteps * (slice + 1) / p.slices;
     constexpr int kWide = kMode == kShrink ? 64 : 32;
-    const int64_t ksteps = (p.K + kWide - 1) / kWide, k_begin = ksteps * rank / kLoraCluster, k_end = ksteps * (rank + 1) / kLoraCluster;
+    const int64_t ksteps = (p.K + kWide - 1) / kWide, k_begin = ksteps * rank >> log2_cluster, k_end = ksteps * (rank + 1) >> log2_cluster;
     for (int i = threadIdx.x; i < kRows; i += kLoraThreads) {
         int64_t m = -1;
         if (i < ch.rows) m = p.row_index ? static_cast<int64_t>(__ldcg(p.row_index + ch.row0 + i)) : ch.row0 + i;
@@ -429,20 +430,23 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
     }
     if constexpr (kMode != kExpand) {
         // Entries in pairs: sum over the cluster, times scale, in bf16 parts. A chunk of 16 rows is small enough for every CTA to
-        // sum all of it for itself; of 64 rows each sums an eighth, for the workspace.
+        // sum all of it for itself; of 64 rows each sums its share, for the workspace.
         constexpr bool kAll = kMode == kFused;
         cluster_sync();
         const float scale = p.scale ? __ldg(p.scale + ch.a) : 1.0f;
-        const int pairs = (kAll ? ch.rows : kRows) * r / 2, at0 = kAll ? 0 : rank * pairs / kLoraCluster,
-                  at1 = kAll ? pairs : (rank + 1) * pairs / kLoraCluster;
+        const int pairs = (kAll ? ch.rows : kRows) * r / 2, at0 = kAll ? 0 : rank * pairs >> log2_cluster,
+                  at1 = kAll ? pairs : (rank + 1) * pairs >> log2_cluster;
         for (int i = at0 + threadIdx.x; i < at1; i += kLoraThreads) {
             float a0[kLoraCluster], a1[kLoraCluster], v0 = 0.0f, v1 = 0.0f;
 #pragma unroll
-            for (int c = 0; c < kLoraCluster; ++c)
+            for (int c = 0; c < kLoraCluster; ++c) {
+                a0[c] = a1[c] = 0.0f;
+                if (c >= cluster) continue;
                 asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
                              : "=f"(a0[c]), "=f"(a1[c])
                              : "r"(map_to_rank(smem_u32(mine + 2 * i), c))
                              : "memory");
+            }
 #pragma unroll
             for (int c = 0; c < kLoraCluster; ++c) v0 += a0[c], v1 += a1[c];
             v0 *= scale, v1 *= scale;

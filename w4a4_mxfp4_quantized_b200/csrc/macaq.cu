@@ -1240,14 +1240,17 @@ macaq_status launch_lora(LoraArgs g, int64_t chunks, int64_t slices, cudaStream_
     g.slices = static_cast<int32_t>(slices);
     if (chunks * slices >= (int64_t(1) << 31)) return MACAQ_ERR_SHAPE;
     return launch(k, dim3(static_cast<unsigned>(chunks * slices)), dim3(kLoraThreads), smem, st,
-                  kMode == kExpand ? 1 : kLoraCluster, g);
+                  kMode == kExpand ? 1 : (kMode == kShrink ? static_cast<int>(slices) : kLoraCluster), g);
 }
 
 template <int kSteps, bool kF32>
 macaq_status run_lora(const LoraArgs &g, const LoraPlan &p, int sms, cudaStream_t st) {
     const int64_t nsteps = (g.N + 31) / 32;
     if (p.wide) {
-        const macaq_status s = launch_lora<kSteps, kF32, kShrink>(g, p.chunks, kLoraCluster, st);
+        // K is split as far as one round of two CTAs per SM goes
+        int64_t split = kLoraCluster;
+        while (split > 1 && p.chunks * split > 2 * sms) split /= 2;
+        const macaq_status s = launch_lora<kSteps, kF32, kShrink>(g, p.chunks, split, st);
         if (s != MACAQ_OK) return s;
         // slices of at least one step per warp, for one round of two CTAs per SM (what comes before a CTA's first step, about
         // 5 us, is paid once)
