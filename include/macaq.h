@@ -275,7 +275,7 @@ macaq_status macaq_row_groups(const int32_t *ids, int64_t T, int32_t topk, int32
 
 /*
  * A whole mixture-of-experts layer for few tokens (decode), in the weight-only mode: MXFP4 weights,
- * bf16 activations, two launches.
+ * bf16 activations, three launches.
  *     x' = X[t] diag(inv_s_gu[e]) H_b;   G, U = x' dq(W'_gu[e])^T  (64-row interleaved, as macaq_linear_swiglu)
  *     h' = (silu(G) U) diag(inv_s_down[e]) H_b';   y_r = h' dq(W'_down[e])^T
  *     out[t] = bf16( sum over j of weights[t, j] * y_{pos[t, j]} ),  fp32 accumulation
@@ -310,8 +310,8 @@ macaq_status macaq_moe_w4a16(const void *X, int64_t T, int64_t K, const float *w
  * Low-rank adapters of many requests beside a shared projection:
  *     out[m] = Y[m] + scale[a] * (X[m] A[a]^T) B[a]^T      for the rows m of adapter a
  * with fp32 sums, rounded to out's type. X A^T is held in all of fp32's bits for fp32 outputs; for bf16 outputs in 16
- * bits, and in bf16 where the call has many rows (over some 600, and over 32 per adapter), which leaves it 2^-9 off:
- * below the output's own rounding.
+ * bits, and in bf16 where the call has many rows (at least 16 per adapter, 32 for ranks up to 32, and enough of them for the
+ * width), which leaves it 2^-9 off: below the output's own rounding.
  * Y is the projection's output, from any of the linear calls; X its input (before the activation transform).
  *   Y, out         device [M, N], bf16 or fp32 per dtype (MACAQ_OUT_BF16 / MACAQ_OUT_F32), rows ldy and ldo
  *                  elements apart (>= N): a column slice of a fused projection is fine. out == Y (with
@@ -324,7 +324,7 @@ macaq_status macaq_moe_w4a16(const void *X, int64_t T, int64_t K, const float *w
  *                  (macaq_row_groups with topk = 1). row_index lists every row once: a row listed twice
  *                  gets one of the two results. NULL row_index: the rows are sorted already. Read on the
  *                  device; out-of-range values are clamped or skipped.
- *   workspace      at least macaq_lora_workspace_bytes(M, r, L, dtype) bytes (0 for few rows: may be NULL then);
+ *   workspace      at least macaq_lora_workspace_bytes(M, r, L, dtype) bytes (0 for few rows per adapter: may be NULL then);
  *                  no initial value needed, nothing kept between calls. Calls that may overlap need separate ones.
  *   K, N, r, ldx, ldy, ldo multiples of 8 (ldy, ldo of fp32: 4); 8 <= r <= 128; 1 <= L <= 1024; M >= 0
  *   (0: no-op), M < 2^31; K, N <= 2^24. Every pointer 16-byte aligned, scale 4-byte.

@@ -157,6 +157,19 @@ def test_many_rows_in_two_launches(r, dtype):
     assert bool(((apart.double() - want).abs() <= bound).all())
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,K,N,r,L", [(16, 72, 20008, 128, 1), (33, 520, 14336, 64, 2), (65, 8, 12000, 24, 1), (100, 4104, 4104, 96, 3)])
+def test_two_launches_for_few_rows_on_many_columns(M, K, N, r, L, dtype):
+    check(make(M, M, K, N, r, L, dtype))
+
+
+@pytest.mark.parametrize("M", [2100, 4100, 8200, 20100])
+@pytest.mark.parametrize("K,r", [(72, 8), (584, 64)])
+def test_clusters_of_eight_to_one(M, K, r):
+    """Fewer CTAs per chunk as the chunks grow in number; K narrower than all of them take, and with a ragged end."""
+    check(make(M, M, K, 136, r, 3, torch.bfloat16))
+
+
 def test_two_calls_at_once():
     """The two-launch form on two streams at the same time, each with its own workspace."""
     cs = [make(s, 1500, 512, 1024, 16, 4, torch.bfloat16) for s in (1, 2)]

@@ -1209,26 +1209,36 @@ macaq_status moe_w4a16(const MoeArgs &a, void *workspace, size_t ws_bytes, cudaS
 }
 
 // ------------------------------------------------------------------------ low-rank adapters
-constexpr int64_t kLoraNarrowChunks = 37;   // 16-row chunks up to which no others are used
+constexpr int64_t kLoraRounds = 74;            // 16-row chunks of two rounds of clusters of eight (two CTAs per SM)
+constexpr int64_t kLoraNarrowWork = 2500000;   // 16-row chunks times entries of an adapter's B
 
-// How a call is cut. 16-row chunks while one round of clusters takes them all (37 of eight CTAs, two per SM): 400 rows of 4
-// adapters, rank 64, 4096 -> 14336, take 24 us against 28 us in 64-row chunks. Beyond, 64-row chunks where adapters have more
-// than 32 rows, since A and B are read per chunk: 700 rows of 8 adapters, rank 32, 26 against 32 us; 2048 of 40, rank 16, 55
-// against 68 us. Those take two launches: 33.6 against 45.2 us in one for 1000 rows of 4 adapters, rank 64.
+// How a call is cut. In 16-row chunks (one launch) B is read and multiplied for every 16 rows, in 64-row chunks (two launches) a
+// quarter as often, where adapters have the rows to fill them. 4096 -> 14336, bf16: 64 rows of one adapter take 7.6 (16-row
+// chunks) against 7.9 us with rank 16 (1.4 M), 12.4 against 10.3 us with rank 64 (5.5 M), 256 rows 16.8 against 13.8 us; 4096
+// -> 1024: 128 rows of rank 64 8.2 against 9.7 us (0.7 M), 512 rows of 8 adapters 14.4 against 13.7 us (2.7 M), 1000 rows of
+// 16 adapters of rank 16 15.8 against 13.0 us (80 chunks). With 16 rows per adapter rank 16 is faster in 16-row chunks (512 rows
+// on 1024 columns 11.6 against 12.8 us, fp32 12.2 against 15.0), rank 64 in 64-row chunks (19.1 against 17.2, 25.8 against 18.9).
 struct LoraPlan {
     bool wide;
     int64_t chunks;
-    size_t ws_bytes;
 };
 
-LoraPlan lora_plan(int64_t M, int32_t L, int32_t r, bool f32) {
+bool lora_fills_chunks(int64_t M, int32_t L, int32_t r) { return M >= (r > 32 ? 16 : 32) * static_cast<int64_t>(L); }
+
+// One chunk per adapter with rows and one for the rows of none, one more per `rows` rows.
+int64_t lora_chunks(int64_t M, int32_t L, int rows) { return std::min<int64_t>(L + 1, M) + M / rows; }
+
+LoraPlan lora_plan(int64_t M, int32_t L, int32_t r, int64_t N) {
+    const int64_t narrow = lora_chunks(M, L, 16);
     LoraPlan p;
-    p.wide = std::min<int64_t>(L + 1, M) + M / 16 > kLoraNarrowChunks && M > 32 * static_cast<int64_t>(L);
-    const int rows = p.wide ? 64 : 16;
-    // one chunk per adapter with rows and one for the rows of none, one more per `rows` rows
-    p.chunks = std::min<int64_t>(L + 1, M) + M / rows;
-    p.ws_bytes = p.wide ? static_cast<size_t>(p.chunks) * lora_v_bytes(r, 4, lora_parts(4, f32)) : 0;
+    p.wide = lora_fills_chunks(M, L, r) && (narrow > kLoraRounds || narrow * N * r > kLoraNarrowWork);
+    p.chunks = p.wide ? lora_chunks(M, L, 64) : narrow;
     return p;
+}
+
+// For every N.
+size_t lora_workspace_bytes(int64_t M, int32_t L, int32_t r, bool f32) {
+    return lora_fills_chunks(M, L, r) ? static_cast<size_t>(lora_chunks(M, L, 64)) * lora_v_bytes(r, 4, lora_parts(4, f32)) : 0;
 }
 
 template <int kSteps, bool kF32, LoraMode kMode>
@@ -1279,8 +1289,9 @@ macaq_status lora_add(const LoraArgs &p, int32_t dtype, void *workspace, size_t 
         !aligned16(p.row_index) || !aligned4(p.scale) || !aligned16(workspace))
         return MACAQ_ERR_ALIGNMENT;
     const bool f32 = dtype == MACAQ_OUT_F32;
-    const LoraPlan plan = lora_plan(p.M, p.L, p.r, f32);
-    if (plan.ws_bytes > 0 && (workspace == nullptr || ws_bytes < plan.ws_bytes)) return MACAQ_ERR_WORKSPACE;
+    const LoraPlan plan = lora_plan(p.M, p.L, p.r, p.N);
+    const size_t need = lora_workspace_bytes(p.M, p.L, p.r, f32);
+    if (need > 0 && (workspace == nullptr || ws_bytes < need)) return MACAQ_ERR_WORKSPACE;
     DeviceInfo dev;
     macaq_status s = device_info(&dev);
     if (s != MACAQ_OK) return s;
@@ -1552,7 +1563,7 @@ macaq_status macaq_lora_add(const void *Y, int64_t ldy, void *out, int64_t ldo, 
 size_t macaq_lora_workspace_bytes(int64_t M, int32_t r, int32_t L, int32_t dtype) {
     if (M <= 0 || M >= (int64_t(1) << 31) || L < 1 || L > macaq::kRouteMaxExperts || r < 8 || r > macaq::kLoraMaxRank || r % 8)
         return 0;
-    return macaq::lora_plan(M, L, r, dtype == MACAQ_OUT_F32).ws_bytes;
+    return macaq::lora_workspace_bytes(M, L, r, dtype == MACAQ_OUT_F32);
 }
 
 }  // extern "C"
