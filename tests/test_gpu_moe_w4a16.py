@@ -83,6 +83,11 @@ def test_widest_layers(T, E, topk, K, I):
     check(tokens(T + K, T, K), *routing(E + T, T, E, topk), layer_of(T + E + K, E, K, I, 256))
 
 
+@pytest.mark.parametrize("T,E,topk", [(4, 1024, 3), (64, 1024, 8), (64, 64, 32), (64, 32, 32), (1, 1, 1)])
+def test_most_experts_and_choices(T, E, topk):
+    check(tokens(T + E, T, 128), *routing(E + T, T, E, topk, drop=0.1), layer_of(T + E, E, 128, 128, 128))
+
+
 @pytest.mark.parametrize("b", [1, 16, 32, 64, 128])
 @pytest.mark.parametrize("b_dn", [1, 16, 32, 64, 128])
 def test_hadamard_blocks(b, b_dn):
