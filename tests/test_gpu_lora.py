@@ -125,6 +125,17 @@ def test_bad_plans_stay_inside_the_buffers():
     assert o.intact()
 
 
+def test_overlapping_groups_in_two_launches_stay_inside_the_workspace():
+    """Offsets that go back and forth: more chunks than a sound plan of so many rows can have."""
+    M, N, L = 600, 2048, 16
+    c = make(5, M, 128, N, 64, L, torch.bfloat16)
+    off = torch.tensor([0, M] * (L // 2) + [0], dtype=torch.int32, device="cuda")
+    y, ws = Guarded(M * N * 2, dtype=torch.bfloat16, shape=(M, N)), Guarded(mq.lora_workspace_bytes(M, 64, L))
+    mq.lora_add(c["Y"], c["X"], c["A"], c["B"], off, out=y.t, workspace=ws.t)
+    torch.cuda.synchronize()
+    assert y.intact() and ws.intact()
+
+
 def test_an_infinity_stays_one():
     """X A^T beyond the parts' range: the output is the infinity that the formula gives, not NaN."""
     for M, dtype in ((3, torch.bfloat16), (3, torch.float32), (200, torch.bfloat16), (1500, torch.float32)):
