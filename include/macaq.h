@@ -275,7 +275,7 @@ macaq_status macaq_row_groups(const int32_t *ids, int64_t T, int32_t topk, int32
 
 /*
  * A whole mixture-of-experts layer for few tokens (decode), in the weight-only mode: MXFP4 weights,
- * bf16 activations, three launches.
+ * bf16 activations, three launches (two for few rows).
  *     x' = X[t] diag(inv_s_gu[e]) H_b;   G, U = x' dq(W'_gu[e])^T  (64-row interleaved, as macaq_linear_swiglu)
  *     h' = (silu(G) U) diag(inv_s_down[e]) H_b';   y_r = h' dq(W'_down[e])^T
  *     out[t] = bf16( sum over j of weights[t, j] * y_{pos[t, j]} ),  fp32 accumulation

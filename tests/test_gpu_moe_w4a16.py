@@ -72,12 +72,14 @@ def routing(seed, T, E, topk, drop=0.0):
 @pytest.mark.parametrize("T,E,topk,K,I,N", [(1, 8, 2, 256, 128, 256), (1, 128, 8, 512, 256, 512), (3, 4, 1, 128, 128, 128),
                                             (17, 6, 3, 384, 640, 128), (64, 16, 4, 256, 256, 384), (64, 1, 1, 128, 128, 128),
                                             (33, 300, 6, 128, 128, 128), (5, 2, 2, 2048, 768, 2048), (9, 3, 2, 4224, 128, 128),
-                                            (2, 3, 3, 128, 2176, 256)])
+                                            (2, 3, 3, 128, 2176, 256), (8, 40, 2, 256, 384, 128), (8, 3, 2, 128, 128, 4736),
+                                            (2, 4, 2, 256, 128, 4864), (16, 9, 1, 128, 256, 256), (17, 9, 1, 128, 256, 256)])
 def test_sizes(T, E, topk, K, I, N):
     check(tokens(T + K, T, K), *routing(E + T, T, E, topk), layer_of(T + E + K, E, K, I, N))
 
 
-@pytest.mark.parametrize("T,E,topk,K,I", [(9, 2, 2, 16384, 128), (9, 3, 1, 128, 16384), (40, 2, 1, 16384, 128), (30, 2, 2, 128, 8192)])
+@pytest.mark.parametrize("T,E,topk,K,I", [(9, 2, 2, 16384, 128), (9, 3, 1, 128, 16384), (40, 2, 1, 16384, 128), (30, 2, 2, 128, 8192),
+                                          (2, 2, 1, 128, 16384), (1, 3, 3, 256, 15872)])
 def test_widest_layers(T, E, topk, K, I):
     """Panels of so many channels that few rows fit: smaller chunks, and several phases per CTA."""
     check(tokens(T + K, T, K), *routing(E + T, T, E, topk), layer_of(T + E + K, E, K, I, 256))

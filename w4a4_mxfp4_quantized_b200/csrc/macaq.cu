@@ -1152,23 +1152,24 @@ bool moe_w4a16_shape_ok(int64_t T, int32_t topk, int32_t E, int64_t K, int64_t I
            N <= (int64_t(1) << 20);
 }
 
+constexpr int kMoeSmem = 232448 - 4 * 1024;   // of an SM, less the static arrays
+
 // Kernel 1 or 2, with column tiles for 8 kNt rows.
 template <bool kDown, int kNt>
 macaq_status moe_launch(MoeArgs g, int sms, cudaStream_t st) {
-    constexpr int kSmem = 232448 - 4 * 1024;   // of an SM, less the static arrays
     constexpr int kTable = 1024;   // room for the chunk table: a CTA meets a few chunks
     const int tiles = (kDown ? g.I : g.K) / 128;
     const int64_t per_chunk = (kDown ? g.N : 2 * g.I) / 32;
     // panel rows: what fits; a chunk has no more rows than that
     const int fixed = moe_table_offset(kNt, tiles, 0) + kTable;
-    g.panel_rows = std::min((kSmem - fixed) / moe_row_bytes(tiles), kMoeMaxPanels * 8 * kNt);
+    g.panel_rows = std::min((kMoeSmem - fixed) / moe_row_bytes(tiles), kMoeMaxPanels * 8 * kNt);
     if (g.panel_rows < 1) return MACAQ_ERR_SHAPE;
     g.chunk_rows = std::min(8 * kNt, g.panel_rows);
     const int64_t chunks = std::min(g.E, g.R) + g.R / g.chunk_rows, items = chunks * per_chunk;
     const int64_t ctas = std::min<int64_t>(items, sms);
     g.max_chunks = static_cast<int32_t>((items + ctas - 1) / ctas / per_chunk + 2);
     const size_t smem = moe_table_offset(kNt, tiles, g.panel_rows) + g.max_chunks * sizeof(MoeChunk);
-    if (smem > kSmem) return MACAQ_ERR_SHAPE;
+    if (smem > kMoeSmem) return MACAQ_ERR_SHAPE;
     auto k = moe_w4a16_kernel<kDown, kNt>;
     macaq_status s = set_smem(k, smem);
     if (s != MACAQ_OK) return s;
@@ -1178,7 +1179,20 @@ macaq_status moe_launch(MoeArgs g, int sms, cudaStream_t st) {
 template <int kNt>
 macaq_status moe_run(const MoeArgs &g, int sms, cudaStream_t st) {
     macaq_status s = moe_launch<false, kNt>(g, sms, st);
-    if (s == MACAQ_OK) s = moe_launch<true, kNt>(g, sms, st);
+    if (s != MACAQ_OK) return s;
+    const int tiles = g.I / 128, blocks = g.N / 32;
+    const size_t smem = moe_panels_offset(1) + g.R * (moe_row_bytes(tiles) + tiles * 4 + sizeof(MoeChunk));
+    if (g.R <= kMoeFewRows && g.T <= kMoeFewTokens && blocks <= sms && smem <= kMoeSmem) {   // a cluster per 32 weight rows
+        auto k = moe_down_sum_kernel;
+        if ((s = set_smem(k, smem)) != MACAQ_OK) return s;
+        MoeArgs few = g;
+        few.chunk_rows = 8;
+        few.max_chunks = g.R;
+        int ranks = 1;
+        while (ranks < 8 && 2 * ranks * blocks <= sms) ranks *= 2;
+        return launch(k, dim3(static_cast<unsigned>(blocks * ranks)), dim3(kMoeThreads), smem, st, ranks, few, ranks);
+    }
+    s = moe_launch<true, kNt>(g, sms, st);
     if (s != MACAQ_OK) return s;
     const unsigned warps = static_cast<unsigned>(g.T) * (g.N / 128);
     return launch(moe_sum_kernel, dim3((warps + kMoeSumWarps - 1) / kMoeSumWarps), dim3(32 * kMoeSumWarps), 0, st, 1, g);

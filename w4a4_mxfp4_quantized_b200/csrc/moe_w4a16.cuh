@@ -8,10 +8,11 @@
 // Bound by HBM: every active expert's codes and scales are read once (17/32 byte a weight), and an expert has a handful of
 // rows, so the two products are streams of weights against a small operand that stays in shared memory.
 //
-// Plan. Three launches: gate, up and SwiGLU (kernel 1); down (kernel 2); the weighted sum of each token's choices. The rows
-// of an expert are cut into chunks of up to 8 or 16 (8 when experts average four rows or fewer, so that one n8 tile
-// nearly always does). An item is (chunk, 32 weight rows): rows 8 p + g of each of the four 32-row quarters of a scale
-// tile, so one 16-byte scale chunk serves a lane's four rows, and gate and up rows of a channel meet in one lane.
+// Plan. Three launches: gate, up and SwiGLU (kernel 1); down (kernel 2); the weighted sum of each token's choices (for few
+// rows one kernel does the last two, see moe_down_sum_kernel). The rows of an expert are cut into chunks of up to 8 or 16 (8
+// when experts average four rows or fewer, so that one n8 tile nearly always does). An item is (chunk, 32 weight rows):
+// rows 8 p + g of each of the four 32-row quarters of a scale tile, so one 16-byte scale chunk serves a lane's four rows,
+// and gate and up rows of a channel meet in one lane.
 // CTAs, one per SM, take equal contiguous ranges of the items, chunk by chunk, and cut theirs into equal runs of K tiles
 // (128 channels), one per warp, wherever the cuts fall: every warp streams the same number of weights, for one token as
 // for 64. The pieces of a cut item meet in shared memory once the CTA's warps are done. The chunks' operands are
@@ -28,7 +29,7 @@
 // without looking at them; otherwise 1/s joins the weights' scale of the group. fp16's 11 bits round x' and h' 8 times
 // finer than the output's bf16.
 //
-// Measured on B200 (128 experts, top-8, 2048 x 768; a graph that cycles three layers): one token 16.0 us (20.2 MB), 8 tokens
+// Measured on B200 (128 experts, top-8, 2048 x 768; a graph that cycles three layers): one token 15.7 us (20.2 MB), 8 tokens
 // 35.5 us (130 MB), 64 tokens 72.2 us (318 MB, 4.4 TB/s). With 64 tokens the two weight streams themselves run at 5.9 and
 // 5.8 TB/s (36 and 18 us) of the 6.5 that a copy reaches; the rest is three starts (plan 1.3 us, first loads and panel 3 to
 // 5 us, a launch's end to the next one's first instruction 1 to 1.5 us) and the closing of cut items (1 us). One token
@@ -53,6 +54,7 @@ constexpr int kMoeWarps = kMoeThreads / 32;
 constexpr int kMoeStages = 3;
 constexpr int kMoeStageBytes = 2048 + 128;  // 32 rows x 64 code bytes, 8 scale chunks
 constexpr int kMoeMaxPanels = 8;
+constexpr int kMoeFewRows = 16, kMoeFewTokens = 8;   // of moe_down_sum_kernel
 constexpr int kMoeGroupUnroll = 4;         // MX groups of a tile in straight code
 
 struct MoeArgs {
@@ -356,7 +358,9 @@ __device__ __forceinline__ void moe_fill_panels(const MoeArgs &a, const MoeChunk
     if (first) after_loads();
 }
 
-// The weight stream of one warp: the K tiles of consecutive items. issue() starts the copies of the next tile.
+// The weight stream of one warp: the K tiles of consecutive items, or (kAcross) of the same weight rows of consecutive chunks.
+// issue() starts the copies of the next tile.
+template <bool kAcross>
 struct MoeStream {
     const uint8_t *wq, *wsf;
     const MoeChunk *table;
@@ -391,8 +395,8 @@ struct MoeStream {
             --left;
             if (++tile == tiles) {
                 tile = 0;
-                if (++r == per_chunk) {
-                    r = 0;
+                if (kAcross || ++r == per_chunk) {
+                    if (!kAcross) r = 0;
                     ++z;
                 }
                 if (left > 0) point();
@@ -442,7 +446,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_w4a16_kernel(MoeArgs a) {
     int32_t *flags = reinterpret_cast<int32_t *>(s_moe + moe_flags_offset(kNt, kt, a.panel_rows));
     MoeChunk *table = reinterpret_cast<MoeChunk *>(s_moe + moe_table_offset(kNt, kt, a.panel_rows));
 
-    MoeStream w;
+    MoeStream<false> w;
     w.wq = kDown ? a.wq_dn : a.wq_gu;
     w.wsf = kDown ? a.wsf_dn : a.wsf_gu;
     w.table = table;
@@ -577,6 +581,144 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_w4a16_kernel(MoeArgs a) {
         from = to;
         if (from < end) __syncthreads();   // panels and pieces are read before the next phase writes them
     }
+}
+
+// Down and the weighted sum in one launch, for few rows: a cluster of `ranks` CTAs has 32 weight rows of every chunk's expert
+// and sums its outputs over the chunks itself. The K tiles of all chunks, one chunk after the other, are cut into equal
+// runs for the cluster's warps; a warp adds its pieces, times the rows' weights, to sums of its own per token, which
+// meet through shared memory, then through distributed shared memory, always in the same order. It saves a launch, 2 us of the
+// host's time, and for one token some of the GPU's (top-8: 15.7 against 16.0 us; two experts of 4096 x 2048 17.1 against 18.1);
+// but every CTA makes the panels of all its chunks, so that with 24 rows it is slower (25.1 against 23.9), with 16 even.
+__global__ void __launch_bounds__(kMoeThreads, 1) moe_down_sum_kernel(MoeArgs a, int ranks) {
+    extern __shared__ __align__(128) uint8_t s_moe[];
+    __shared__ MoeRow s_rows[kMoeFewRows];
+    __shared__ int32_t s_token[kMoeFewRows];   // of a sorted row, -1 for none
+    __shared__ float s_weight[kMoeFewRows];
+    __shared__ __align__(8) float s_sum[kMoeFewTokens * 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    griddep_launch_dependents();   // kernel 1 has waited for everything before it: the plan and the weights are complete
+    const int rank = blockIdx.x % ranks, item = blockIdx.x / ranks;
+    const int kt = a.I / 128, stride = moe_panel_stride(kt);
+    float *part = reinterpret_cast<float *>(s_moe + moe_heads_offset()) + warp * kMoeFewTokens * 32;   // [token][weight row]
+    uint8_t *panel = s_moe + moe_panels_offset(1);
+    float *xs = reinterpret_cast<float *>(panel + a.R * stride);
+    int32_t *flags = reinterpret_cast<int32_t *>(panel + a.R * moe_row_bytes(kt));   // [chunk][tile]
+    MoeChunk *table = reinterpret_cast<MoeChunk *>(flags + a.R * kt);
+    if (threadIdx.x < kMoeFewRows) {
+        s_rows[threadIdx.x] = {0, 0};
+        s_token[threadIdx.x] = -1;
+    }
+    for (int i = threadIdx.x; i < a.R * kt; i += kMoeThreads) flags[i] = 0;
+    for (int i = lane; i < kMoeFewTokens * 32; i += 32) part[i] = 0.0f;
+
+    int begin, chunks, none;
+    moe_find_items(a, 0, 1, 1, reinterpret_cast<int32_t *>(s_moe), table, begin, chunks, none);   // every chunk
+    const int units = chunks * kt, u0 = units * rank / ranks, u1 = units * (rank + 1) / ranks;
+    const int first = u0 + (u1 - u0) * warp / kMoeWarps, last = u0 + (u1 - u0) * (warp + 1) / kMoeWarps;
+    const int z0 = u0 / kt, z1 = u1 > u0 ? (u1 - 1) / kt : z0 - 1;   // the chunks of this CTA
+    int z = first / kt, tile = first - z * kt;
+    MoeStream<true> w;
+    w.wq = a.wq_dn, w.wsf = a.wsf_dn, w.table = table;
+    w.ring = smem_u32(s_moe) + warp * kMoeStages * kMoeStageBytes;
+    w.st = g * 64 + ((t ^ ((g >> 1) & 3)) << 4);
+    w.K = a.I, w.tiles = kt, w.per_chunk = a.N / 32;
+    w.start(z, item, tile, last - first);
+    // panel rows are the chunks' rows, from the first chunk's on (kept in range where a plan's offsets overlap)
+    auto panel_row = [&](int row) { return min(max(row - table[z0].row0, 0), a.R - 1); };
+    for (int i = threadIdx.x; i < (z1 - z0 + 1) * 8; i += kMoeThreads) {
+        const MoeChunk ch = table[z0 + i / 8];
+        if (i % 8 < ch.rows) s_rows[panel_row(ch.row0 + i % 8)] = {i / 8, ch.row0 + i % 8};
+    }
+    const int32_t live = min(max(__ldcg(a.offsets + a.E), 0), a.R);
+    for (int i = threadIdx.x; i < a.R; i += kMoeThreads) {
+        const int32_t row = __ldcg(a.pos + i);
+        if (row >= 0 && row < live) {
+            s_token[row] = i / a.topk;
+            s_weight[row] = __ldcg(a.weights + i);
+        }
+    }
+    griddep_wait();   // kernel 1's rows; out may still be in use
+    __syncthreads();
+    const int rows = z1 < z0 ? 0 : panel_row(table[z1].row0 + table[z1].rows - 1) + 1;
+    moe_fill_panels<true>(a, table + z0, s_rows, rows, panel, xs, flags, [] {});
+    __syncthreads();
+
+    float acc[2][1][4] = {};
+    const uint8_t *bcol[1];
+    const float *x0[1], *x1[1];
+    const uint32_t ld = (lane >> 3) * 512 + (lane & 7) * 64 + (((lane >> 1) & 3) << 4);
+    auto open = [&]() {
+        const int base = table[z].row0, most = table[z].rows - 1;
+        bcol[0] = panel + panel_row(base + min(g, most)) * stride + t * 16;
+        x0[0] = xs + panel_row(base + min(2 * t, most)) * kt * 4;
+        x1[0] = xs + panel_row(base + min(2 * t + 1, most)) * kt * 4;
+    };
+    if (first < last) open();
+    int slot = 0;
+#pragma unroll 1
+    for (int j = first; j < last; ++j) {
+        cp_async_wait<kMoeStages - 2>();
+        __syncwarp();   // every lane's copies of this tile have landed, and every lane is done with the tile before
+        w.issue();
+        const uint32_t stage = w.ring + slot * kMoeStageBytes;
+        slot = slot == kMoeStages - 1 ? 0 : slot + 1;
+        uint32_t word[4];
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(word[0]), "=r"(word[1]), "=r"(word[2]), "=r"(word[3])
+                     : "r"(stage + 2048 + 16 * g)
+                     : "memory");
+        if (flags[(z - z0) * kt + tile]) moe_tile_mma<1, true>(stage + ld, word, bcol, x0, x1, tile, acc);
+        else moe_tile_mma<1, false>(stage + ld, word, bcol, x0, x1, tile, acc);
+        if (++tile < kt && j + 1 < last) continue;
+        // the end of the chunk or of the run. Row by row, since a token may have chosen an expert twice.
+        const MoeChunk ch = table[z];
+        for (int c = 0; c < ch.rows; ++c) {
+            const int token = s_token[ch.row0 + c];
+            if (t == c >> 1 && token >= 0) {
+                const float weight = s_weight[ch.row0 + c];
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float *at = part + token * 32 + 8 * (2 * m + h) + g;
+                        *at = fmaf(weight, (c & 1) ? acc[m][0][2 * h + 1] : acc[m][0][2 * h], *at);
+                    }
+            }
+            __syncwarp();
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[m][0][k] = 0.0f;
+        tile = 0;
+        ++z;
+        if (j + 1 < last) open();
+    }
+    cp_async_wait<0>();
+    __syncthreads();
+    const float *parts = reinterpret_cast<const float *>(s_moe + moe_heads_offset());
+    if (threadIdx.x < a.T * 32) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int v = 0; v < kMoeWarps; ++v) sum += parts[v * kMoeFewTokens * 32 + threadIdx.x];
+        s_sum[threadIdx.x] = sum;
+    }
+    cluster_sync();
+    if (const int i = threadIdx.x; rank == 0 && i < a.T * 16) {   // two outputs each
+        float v0 = 0.0f, v1 = 0.0f;
+        for (int c = 0; c < ranks; ++c) {
+            float a0, a1;
+            asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                         : "=f"(a0), "=f"(a1)
+                         : "r"(map_to_rank(smem_u32(s_sum + 2 * i), c))
+                         : "memory");
+            v0 += a0, v1 += a1;
+        }
+        const int token = i / 16, q = i % 16 / 4, at = 2 * (i % 4);
+        const __nv_bfloat162 o = __floats2bfloat162_rn(v0, v1);
+        *reinterpret_cast<__nv_bfloat162 *>(a.out + static_cast<int64_t>(token) * a.N + 128 * (item >> 2) + 32 * q + 8 * (item & 3) + at) = o;
+    }
+    cluster_sync();   // no CTA leaves while another reads its sums
 }
 
 // The weighted sum of each token's choices, in the order j = 0, 1, ...: a warp takes 128 outputs of a token.
