@@ -311,7 +311,7 @@ macaq_status macaq_moe_w4a16(const void *X, int64_t T, int64_t K, const float *w
  *     out[m] = Y[m] + scale[a] * (X[m] A[a]^T) B[a]^T      for the rows m of adapter a
  * with fp32 sums, rounded to out's type. X A^T is held in all of fp32's bits for fp32 outputs; for bf16 outputs in 16
  * bits, and in bf16 where the call has many rows (at least 16 per adapter, 32 for ranks up to 32, and enough of them for the
- * width), which leaves it 2^-9 off: below the output's own rounding.
+ * width and rank), which leaves it 2^-9 off: below the output's own rounding.
  * Y is the projection's output, from any of the linear calls; X its input (before the activation transform).
  *   Y, out         device [M, N], bf16 or fp32 per dtype (MACAQ_OUT_BF16 / MACAQ_OUT_F32), rows ldy and ldo
  *                  elements apart (>= N): a column slice of a fused projection is fine. out == Y (with
@@ -324,12 +324,12 @@ macaq_status macaq_moe_w4a16(const void *X, int64_t T, int64_t K, const float *w
  *                  (macaq_row_groups with topk = 1). row_index lists every row once: a row listed twice
  *                  gets one of the two results. NULL row_index: the rows are sorted already. Read on the
  *                  device; out-of-range values are clamped or skipped.
- *   workspace      at least macaq_lora_workspace_bytes(M, r, L, dtype) bytes (0 for few rows per adapter: may be NULL then);
- *                  no initial value needed, nothing kept between calls. Calls that may overlap need separate ones.
+ *   workspace      at least macaq_lora_workspace_bytes(M, K, N, r, L, dtype) bytes (0 where one launch does it: may be NULL
+ *                  then; K or N of 0: enough for every K or N); no initial value needed, nothing kept between calls. Calls that may overlap need separate ones.
  *   K, N, r, ldx, ldy, ldo multiples of 8 (ldy, ldo of fp32: 4); 8 <= r <= 128; 1 <= L <= 1024; M >= 0
  *   (0: no-op), M < 2^31; K, N <= 2^24. Every pointer 16-byte aligned, scale 4-byte.
  */
-size_t macaq_lora_workspace_bytes(int64_t M, int32_t r, int32_t L, int32_t dtype);
+size_t macaq_lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int32_t r, int32_t L, int32_t dtype);
 macaq_status macaq_lora_add(const void *Y, int64_t ldy, void *out, int64_t ldo, int32_t dtype, const void *X, int64_t ldx,
                             int64_t M, int64_t K, int64_t N, const void *A, const void *B, int32_t r, int32_t L,
                             const float *scale, const int32_t *group_offsets, const int32_t *row_index, void *workspace,

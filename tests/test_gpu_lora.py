@@ -127,10 +127,10 @@ def test_bad_plans_stay_inside_the_buffers():
 
 def test_overlapping_groups_in_two_launches_stay_inside_the_workspace():
     """Offsets that go back and forth: more chunks than a sound plan of so many rows can have."""
-    M, N, L = 600, 2048, 16
+    M, N, L = 600, 4096, 16
     c = make(5, M, 128, N, 64, L, torch.bfloat16)
     off = torch.tensor([0, M] * (L // 2) + [0], dtype=torch.int32, device="cuda")
-    y, ws = Guarded(M * N * 2, dtype=torch.bfloat16, shape=(M, N)), Guarded(mq.lora_workspace_bytes(M, 64, L))
+    y, ws = Guarded(M * N * 2, dtype=torch.bfloat16, shape=(M, N)), Guarded(mq.lora_workspace_bytes(M, 64, L, K=128, N=N))
     mq.lora_add(c["Y"], c["X"], c["A"], c["B"], off, out=y.t, workspace=ws.t)
     torch.cuda.synchronize()
     assert y.intact() and ws.intact()
@@ -169,8 +169,9 @@ def test_many_rows_in_two_launches(r, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("M,K,N,r,L", [(16, 72, 20008, 128, 1), (33, 520, 14336, 64, 2), (65, 8, 12000, 24, 1), (100, 4104, 4104, 96, 3)])
+@pytest.mark.parametrize("M,K,N,r,L", [(16, 72, 40008, 128, 1), (33, 520, 40000, 64, 2), (65, 8, 90008, 24, 1), (100, 4104, 10008, 96, 3)])
 def test_two_launches_for_few_rows_on_many_columns(M, K, N, r, L, dtype):
+    assert mq.lora_workspace_bytes(M, r, L, mq.OUT_BF16, K, N) > 0
     check(make(M, M, K, N, r, L, dtype))
 
 

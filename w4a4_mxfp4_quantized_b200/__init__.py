@@ -81,7 +81,7 @@ _SIGNATURES = {
     "macaq_moe_w4a16_workspace_bytes": ([_i64, _i32, _i32, _i64, _i64, _i64], _sz),
     "macaq_moe_w4a16": ([_vp, _i64, _i64, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _vp, _vp, _vp, _i32,
                          _i64, _vp, _vp, _sz, _vp], ctypes.c_int),
-    "macaq_lora_workspace_bytes": ([_i64, _i32, _i32, _i32], _sz),
+    "macaq_lora_workspace_bytes": ([_i64, _i64, _i64, _i32, _i32, _i32], _sz),
     "macaq_lora_add": ([_vp, _i64, _vp, _i64, _i32, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp,
                         _sz, _vp], ctypes.c_int),
 }
@@ -438,8 +438,9 @@ def moe_w4a16(X: torch.Tensor, weights: torch.Tensor, group_offsets: torch.Tenso
 
 
 @functools.lru_cache(maxsize=1024)
-def lora_workspace_bytes(M: int, r: int, L: int, dtype: int = OUT_BF16) -> int:
-    return int(lib().macaq_lora_workspace_bytes(M, r, L, dtype))
+def lora_workspace_bytes(M: int, r: int, L: int, dtype: int = OUT_BF16, K: int = 0, N: int = 0) -> int:
+    """Bytes that lora_add needs; without K or N enough for every one."""
+    return int(lib().macaq_lora_workspace_bytes(M, K, N, r, L, dtype))
 
 
 def _rows(name: str, t: torch.Tensor, dtype, M: int, N: int, dev):
@@ -471,7 +472,7 @@ def lora_add(Y: torch.Tensor, X: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
     xp, ldx = _rows("X", X, torch.bfloat16, M, K, dev)
     bf16, i32 = torch.bfloat16, torch.int32
     if workspace is None:   # of this call alone: calls on other streams and captured graphs have their own
-        need = lora_workspace_bytes(M, r, L, _ROWS_DTYPE[Y.dtype])
+        need = lora_workspace_bytes(M, r, L, _ROWS_DTYPE[Y.dtype], K, N)
         workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
     _call("macaq_lora_add", dev, yp, ldy, op, ldo, _ROWS_DTYPE[Y.dtype], xp, ldx, M, K, N,
           _arg("A", A, bf16, (L, r, K), dev), _arg("B", B, bf16, (L, N, r), dev), r, L,

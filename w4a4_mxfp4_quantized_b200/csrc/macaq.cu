@@ -1223,36 +1223,34 @@ macaq_status moe_w4a16(const MoeArgs &a, void *workspace, size_t ws_bytes, cudaS
 }
 
 // ------------------------------------------------------------------------ low-rank adapters
-constexpr int64_t kLoraRounds = 74;            // 16-row chunks of two rounds of clusters of eight (two CTAs per SM)
-constexpr int64_t kLoraNarrowWork = 2500000;   // 16-row chunks times entries of an adapter's B
+constexpr int64_t kLoraRounds = 74;             // 16-row chunks of two rounds of clusters of eight (two CTAs per SM)
+constexpr int64_t kLoraNarrowWork = 12000000;   // 16-row chunks times entries of an adapter's A and B
 
-// How a call is cut. In 16-row chunks (one launch) B is read and multiplied for every 16 rows, in 64-row chunks (two launches) a
-// quarter as often, where adapters have the rows to fill them. 4096 -> 14336, bf16: 64 rows of one adapter take 7.6 (16-row
-// chunks) against 7.9 us with rank 16 (1.4 M), 12.4 against 10.3 us with rank 64 (5.5 M), 256 rows 16.8 against 13.8 us; 4096
-// -> 1024: 128 rows of rank 64 8.2 against 9.7 us (0.7 M), 512 rows of 8 adapters 14.4 against 13.7 us (2.7 M), 1000 rows of
-// 16 adapters of rank 16 15.8 against 13.0 us (80 chunks). With 16 rows per adapter rank 16 is faster in 16-row chunks (512 rows
-// on 1024 columns 11.6 against 12.8 us, fp32 12.2 against 15.0), rank 64 in 64-row chunks (19.1 against 17.2, 25.8 against 18.9).
+// How a call is cut. In 16-row chunks (one launch) A and B are read and multiplied for every 16 rows, in 64-row chunks (two
+// launches) a quarter as often, where adapters have the rows to fill them. bf16, 4 adapters, in 16-row against 64-row chunks:
+// 4096 -> 14336, rank 64, 64 rows (11 M) 13.0 against 10.6 us, 128 rows (15 M) 16.2 against 11.2, 256 rows 22.7 against 16.3;
+// 4096 -> 1024, rank 64, 512 rows (12 M) 11.8 against 11.7 us, rank 128, 256 rows (14 M) 19.1 against 13.9; 1000 rows of 16
+// adapters of rank 16 (80 chunks) 15.8 against 13.0 us. Two launches take 16 us of the host's time from Python, one 10, so
+// that calls under some 14 us stay with one. With 16 rows per adapter rank 16 is faster in 16-row chunks (512 rows on
+// 1024 columns 11.6 against 12.8 us, fp32 12.2 against 15.0), rank 64 in 64-row chunks (19.1 against 17.2, 25.8 against 18.9).
 struct LoraPlan {
     bool wide;
     int64_t chunks;
 };
 
-bool lora_fills_chunks(int64_t M, int32_t L, int32_t r) { return M >= (r > 32 ? 16 : 32) * static_cast<int64_t>(L); }
-
 // One chunk per adapter with rows and one for the rows of none, one more per `rows` rows.
 int64_t lora_chunks(int64_t M, int32_t L, int rows) { return std::min<int64_t>(L + 1, M) + M / rows; }
 
-LoraPlan lora_plan(int64_t M, int32_t L, int32_t r, int64_t N) {
+LoraPlan lora_plan(int64_t M, int32_t L, int32_t r, int64_t K, int64_t N) {
     const int64_t narrow = lora_chunks(M, L, 16);
     LoraPlan p;
-    p.wide = lora_fills_chunks(M, L, r) && (narrow > kLoraRounds || narrow * N * r > kLoraNarrowWork);
+    p.wide = M >= (r > 32 ? 16 : 32) * static_cast<int64_t>(L) && (narrow > kLoraRounds || narrow * r * (K + N) > kLoraNarrowWork);
     p.chunks = p.wide ? lora_chunks(M, L, 64) : narrow;
     return p;
 }
 
-// For every N.
-size_t lora_workspace_bytes(int64_t M, int32_t L, int32_t r, bool f32) {
-    return lora_fills_chunks(M, L, r) ? static_cast<size_t>(lora_chunks(M, L, 64)) * lora_v_bytes(r, 4, lora_parts(4, f32)) : 0;
+size_t lora_workspace_bytes(const LoraPlan &p, int32_t r, bool f32) {
+    return p.wide ? static_cast<size_t>(p.chunks) * lora_v_bytes(r, 4, lora_parts(4, f32)) : 0;
 }
 
 template <int kSteps, bool kF32, LoraMode kMode>
@@ -1303,8 +1301,8 @@ macaq_status lora_add(const LoraArgs &p, int32_t dtype, void *workspace, size_t 
         !aligned16(p.row_index) || !aligned4(p.scale) || !aligned16(workspace))
         return MACAQ_ERR_ALIGNMENT;
     const bool f32 = dtype == MACAQ_OUT_F32;
-    const LoraPlan plan = lora_plan(p.M, p.L, p.r, p.N);
-    const size_t need = lora_workspace_bytes(p.M, p.L, p.r, f32);
+    const LoraPlan plan = lora_plan(p.M, p.L, p.r, p.K, p.N);
+    const size_t need = lora_workspace_bytes(plan, p.r, f32);
     if (need > 0 && (workspace == nullptr || ws_bytes < need)) return MACAQ_ERR_WORKSPACE;
     DeviceInfo dev;
     macaq_status s = device_info(&dev);
@@ -1574,10 +1572,12 @@ macaq_status macaq_lora_add(const void *Y, int64_t ldy, void *out, int64_t ldo, 
     return macaq::lora_add(p, dtype, workspace, ws_bytes, static_cast<cudaStream_t>(stream));
 }
 
-size_t macaq_lora_workspace_bytes(int64_t M, int32_t r, int32_t L, int32_t dtype) {
+size_t macaq_lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int32_t r, int32_t L, int32_t dtype) {
     if (M <= 0 || M >= (int64_t(1) << 31) || L < 1 || L > macaq::kRouteMaxExperts || r < 8 || r > macaq::kLoraMaxRank || r % 8)
         return 0;
-    return macaq::lora_workspace_bytes(M, L, r, dtype == MACAQ_OUT_F32);
+    constexpr int64_t kMost = int64_t(1) << 24;
+    if (K < 0 || K > kMost || N < 0 || N > kMost) return 0;
+    return macaq::lora_workspace_bytes(macaq::lora_plan(M, L, r, K == 0 ? kMost : K, N == 0 ? kMost : N), r, dtype == MACAQ_OUT_F32);
 }
 
 }  // extern "C"
