@@ -462,9 +462,8 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
                 else *reinterpret_cast<uint32_t *>(p.v + static_cast<int64_t>(z) * kParts * kRows * vs + at) = w;
             }
         }
-        __syncwarp();
         if constexpr (kAll) {
-            asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // waited for at the end
+            cluster_arrive();   // waited for at the end
             __syncthreads();
         } else {
             cluster_sync();   // no CTA leaves while another reads its sums
@@ -532,8 +531,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
         if constexpr (kMt > 1) load_b(s + kLoraWarps, b);
     }
     if constexpr (kMode == kFused) {
-        __syncwarp();
-        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // no CTA leaves while another reads its sums
+        cluster_wait();   // no CTA leaves while another reads its sums
     }
 }
 

@@ -316,8 +316,19 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
     return r;
 }
 
+// The barrier of a cluster's threads. Its aligned form needs every lane of the warp at the same instruction; lanes that
+// come out of different branches or loops are only brought together by __syncwarp.
+__device__ __forceinline__ void cluster_arrive() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
 }
 
 // Address of the same shared-memory variable in CTA `rank` of the cluster.

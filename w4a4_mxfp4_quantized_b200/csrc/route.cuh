@@ -225,8 +225,7 @@ __global__ void __launch_bounds__(kGroupThreads) row_groups_kernel(RouteArgs t, 
         first[b] = lower;
         sums[b] = all;
     }
-    __syncwarp();
-    if (ctas > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // done with the others' totals
+    if (ctas > 1) cluster_arrive();   // done with the others' totals
     __syncthreads();
     const int b = threadIdx.x;
     const int32_t total = b < a.E ? sums[b] : 0;
@@ -279,8 +278,7 @@ __global__ void __launch_bounds__(kGroupThreads) row_groups_kernel(RouteArgs t, 
             }
         }
     }
-    __syncwarp();
-    if (ctas > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // no CTA leaves while its totals are read
+    if (ctas > 1) cluster_wait();   // no CTA leaves while its totals are read
 }
 
 }  // namespace macaq
