@@ -309,9 +309,8 @@ macaq_status macaq_moe_w4a16(const void *X, int64_t T, int64_t K, const float *w
 /*
  * Low-rank adapters of many requests beside a shared projection:
  *     out[m] = Y[m] + scale[a] * (X[m] A[a]^T) B[a]^T      for the rows m of adapter a
- * with fp32 sums, rounded to out's type. X A^T is held in all of fp32's bits for fp32 outputs; for bf16 outputs in 16
- * bits, and in bf16 where the call has many rows (at least 16 per adapter, 32 for ranks up to 32, and enough of them for the
- * width and rank), which leaves it 2^-9 off: below the output's own rounding.
+ * with fp32 sums, rounded to out's type. X A^T is held in all of fp32's bits for fp32 outputs and in 16 bits for bf16
+ * outputs (off by at most 2^-16 of each of its values), whatever the number of rows.
  * Y is the projection's output, from any of the linear calls; X its input (before the activation transform).
  *   Y, out         device [M, N], bf16 or fp32 per dtype (MACAQ_OUT_BF16 / MACAQ_OUT_F32), rows ldy and ldo
  *                  elements apart (>= N): a column slice of a fused projection is fine. out == Y (with

@@ -1,0 +1,101 @@
+"""Adapters on small integers, where every product and sum is exact in fp32 and X A^T has up to 15 bits: the output has to be
+the formula's value rounded once, bit for bit, also where Y cancels the adapter's share and nothing hides a rounding of X A^T."""
+import pytest
+import torch
+
+import w4a4_mxfp4_quantized_b200 as mq
+from sfutil import Guarded
+
+pytestmark = pytest.mark.gpu
+
+
+def ints(g, bound, *shape):
+    return torch.randint(-bound, bound + 1, shape, generator=g, device="cuda").double()
+
+
+def make(seed, M, K, N, r, L, dtype, absent=0.2):
+    """|X A^T| <= 2^15 and |X A^T B^T| < 2^23 (checked), so that fp32 holds every partial sum; scales are powers of two."""
+    g = torch.Generator("cuda").manual_seed(seed)
+    ids = torch.randint(0, L, (M,), generator=g, device="cuda", dtype=torch.int32)
+    ids[torch.rand(M, generator=g, device="cuda") < absent] = L
+    X, A, B = ints(g, 127, M, K), ints(g, 3, L, r, K), ints(g, 3, L, N, r)
+    scale = torch.tensor([1.0, 0.5, 2.0, -1.0, 4.0], device="cuda")[torch.arange(L, device="cuda") % 5]
+    delta = torch.zeros(M, N, dtype=torch.float64, device="cuda")
+    for a in range(L):
+        rows = torch.nonzero(ids == a).reshape(-1)
+        v = X[rows] @ A[a].T
+        assert rows.numel() == 0 or (v.abs().max() <= 2 ** 15 and (v.abs() @ B[a].abs().T).max() < 2 ** 21)
+        delta[rows] = scale[a].double() * (v @ B[a].T)
+    Y = (-delta).to(dtype)   # cancels the adapter's share but for what bf16 cannot hold
+    Y[::3] = ints(g, 100, Y[::3].shape[0], N).to(dtype)
+    want = (Y.double() + delta).to(dtype)
+    to = lambda t: t.to(torch.bfloat16)  # noqa: E731
+    return dict(X=to(X), A=to(A), B=to(B), Y=Y, scale=scale, ids=ids, want=want, L=L)
+
+
+def two_launches(M, K, N, r, L, dtype):
+    return mq.lora_workspace_bytes(M, r, L, mq.OUT_F32 if dtype == torch.float32 else mq.OUT_BF16, K, N) > 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("r", [8, 16, 24, 40, 64, 72, 104, 128])
+@pytest.mark.parametrize("M", [1, 40, 1500])
+def test_exact(M, r, dtype):
+    c = make(M + r, M, 200, 328, r, 4, dtype)
+    assert two_launches(M, 200, 328, r, 4, dtype) == (M == 1500)
+    off, row, _ = mq.row_groups(c["ids"], 4)
+    out = mq.lora_add(c["Y"], c["X"], c["A"], c["B"], off, row, scale=c["scale"], out=torch.empty_like(c["Y"]))
+    torch.cuda.synchronize()
+    assert torch.equal(out, c["want"])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_row_has_the_same_result_in_a_small_and_a_large_call(dtype):
+    """Few rows go in one launch, many in two: X A^T has the same bits in both."""
+    c = make(5, 1500, 320, 264, 32, 4, dtype, absent=0.0)
+    off, row, _ = mq.row_groups(c["ids"], 4)
+    many = mq.lora_add(c["Y"], c["X"], c["A"], c["B"], off, row, scale=c["scale"], out=torch.empty_like(c["Y"]))
+    for i in (0, 1, 700, 1499):
+        at = slice(i, i + 1)
+        off, row, _ = mq.row_groups(c["ids"][at].clone(), 4)
+        one = mq.lora_add(c["Y"][at].clone(), c["X"][at].clone(), c["A"], c["B"], off, row, scale=c["scale"])
+        torch.cuda.synchronize()
+        assert torch.equal(one[0], many[i])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,r", [(60, 16), (1500, 16), (1500, 64), (1500, 128)])
+def test_column_slices_of_wider_buffers(M, r, dtype):
+    """X, Y and out as slices, each with a row stride of its own, in both launch forms: nothing beside them changes."""
+    K, N, L = 136, 328, 4
+    c = make(M, M, K, N, r, L, dtype)
+    assert two_launches(M, K, N, r, L, dtype) == (M == 1500)
+    off, row, _ = mq.row_groups(c["ids"], L)
+    xw = torch.full((M, 400), float("nan"), device="cuda", dtype=torch.bfloat16)
+    yw = torch.full((M, 1000), 7.0, device="cuda", dtype=dtype)
+    o = Guarded(M * 752 * c["Y"].element_size(), dtype=dtype, shape=(M, 752))
+    o.t.fill_(5.0)
+    xw[:, 64:64 + K] = c["X"]
+    yw[:, 40:40 + N] = c["Y"]
+    mq.lora_add(yw[:, 40:40 + N], xw[:, 64:64 + K], c["A"], c["B"], off, row, scale=c["scale"], out=o.t[:, 16:16 + N])
+    torch.cuda.synchronize()
+    assert o.intact() and bool((o.t[:, :16] == 5).all()) and bool((o.t[:, 16 + N:] == 5).all())
+    assert torch.equal(o.t[:, 16:16 + N], c["want"]) and torch.equal(yw[:, 40:40 + N], c["Y"])
+    mq.lora_add(yw[:, 40:40 + N], xw[:, 64:64 + K], c["A"], c["B"], off, row, scale=c["scale"])   # in place
+    torch.cuda.synchronize()
+    assert torch.equal(yw[:, 40:40 + N], c["want"])
+    assert bool((yw[:, :40] == 7).all()) and bool((yw[:, 40 + N:] == 7).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,r", [(60, 24), (1500, 24), (1500, 96)])
+def test_sorted_rows_without_an_index(M, r, dtype):
+    c = make(M, M, 264, 328, r, 7, dtype)
+    assert two_launches(M, 264, 328, r, 7, dtype) == (M == 1500)
+    order = torch.sort(c["ids"], stable=True).indices
+    off, _, _ = mq.row_groups(c["ids"][order].contiguous(), 7)
+    Y, X, want = c["Y"][order].contiguous(), c["X"][order].contiguous(), c["want"][order]
+    out = mq.lora_add(Y, X, c["A"], c["B"], off, scale=c["scale"], out=torch.empty_like(Y))
+    mq.lora_add(Y, X, c["A"], c["B"], off, scale=c["scale"])
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(Y, want)

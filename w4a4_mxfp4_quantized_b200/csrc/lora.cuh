@@ -21,7 +21,7 @@
 // the sum over k is complete. In the second product the 32 columns of a step are dealt to the four n8 tiles so that a lane
 // ends up with 8 neighbouring columns of a row: Y moves in 16-byte pieces, through a ring of cp.async stages in which each
 // lane reads back what it copied itself (no barrier; the copies of the next steps are in flight while one is added). V is held in
-// up to three bf16 parts (8, 16 or 24 bits).
+// two or three bf16 parts (16 or 24 bits).
 // Measured on B200 (4096 -> 14336, a graph that cycles three batches): one row of rank 16 5.4 us; 64 rows over 32 adapters of
 // rank 16 12.4 us (19.7 MB; find 1.0, V 1.9, cluster sum 2.0, columns 5 us); 2048 rows of 4 adapters of rank 64 40.9 us
 // (142 MB, 3.5 TB/s: 10 us for V, most of it starts and the cluster's sum, and 27 us for the columns, whose warps
@@ -66,10 +66,10 @@ __host__ __device__ constexpr int lora_padded_rank(int r) { return r <= 32 ? 32 
 __host__ __device__ constexpr int lora_v_stride(int r) {   // bf16; 64 bytes off a multiple of 128: no bank conflicts
     return lora_padded_rank(r) == 32 ? 32 : lora_padded_rank(r) + 32;
 }
-// bf16 parts that V is held in: three for fp32 outputs; for bf16 outputs two, and one for chunks of 64 rows, where the
-// second costs a quarter of the launch (2048 rows of rank 64 on 14336 columns: 38 against 29 us) and V's rounding, 2^-9 of
-// the adapter's share, stays under the output's own.
-__host__ __device__ constexpr int lora_parts(int mt, bool f32) { return f32 ? 3 : (mt == 4 ? 1 : 2); }
+// bf16 parts that V is held in: three for fp32 outputs (off by at most 2^-24 of a value), two for bf16 outputs (2^-16), in both
+// forms alike, so that a row's result does not go by the rows beside it. What that leaves in an output is 2^-16 of the sum of
+// |V_j B_j|, also where Y or the terms cancel; one part would leave 2^-8 of it.
+__host__ __device__ constexpr int lora_parts(bool f32) { return f32 ? 3 : 2; }
 __host__ __device__ constexpr int lora_v_bytes(int r, int mt, int parts) { return parts * 16 * mt * lora_v_stride(r) * 2; }
 // The ring of the second product: 16-byte pieces per lane and stage (Y of all rows; for one m16 tile B too), and stages.
 __host__ __device__ constexpr int lora_ring_pieces(int mt, int steps, bool f32) {
@@ -93,7 +93,7 @@ __host__ __device__ constexpr int lora_v_offset(int r, int steps, bool f32, Lora
 }
 __host__ __device__ constexpr int lora_smem_bytes(int r, int steps, bool f32, LoraMode mode) {
     if (mode == kShrink) return lora_shrink_stages(steps) * lora_shrink_stage(steps);
-    return lora_v_offset(r, steps, f32, mode) + lora_v_bytes(r, lora_tiles(mode), lora_parts(lora_tiles(mode), f32));
+    return lora_v_offset(r, steps, f32, mode) + lora_v_bytes(r, lora_tiles(mode), lora_parts(f32));
 }
 
 __device__ __forceinline__ void lora_copy16(uint32_t dst, const void *src, bool on) {   // off: zeros
@@ -192,7 +192,7 @@ struct LoraPiece {
 template <int kSteps, bool kF32, LoraMode kMode>
 __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
     constexpr int kMt = lora_tiles(kMode);   // m16 tiles of a chunk
-    constexpr int kRows = 16 * kMt, kParts = lora_parts(kMt, kF32), kElement = kF32 ? 4 : 2;
+    constexpr int kRows = 16 * kMt, kParts = lora_parts(kF32), kElement = kF32 ? 4 : 2;
     extern __shared__ __align__(16) uint8_t s_lora[];
     __shared__ int32_t s_off[kRouteMaxExperts + 2];
     __shared__ const uint16_t *s_x[kRows];   // the rows' places in X, Y and out, null for none

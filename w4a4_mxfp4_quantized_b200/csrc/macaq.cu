@@ -1250,7 +1250,7 @@ LoraPlan lora_plan(int64_t M, int32_t L, int32_t r, int64_t K, int64_t N) {
 }
 
 size_t lora_workspace_bytes(const LoraPlan &p, int32_t r, bool f32) {
-    return p.wide ? static_cast<size_t>(p.chunks) * lora_v_bytes(r, 4, lora_parts(4, f32)) : 0;
+    return p.wide ? static_cast<size_t>(p.chunks) * lora_v_bytes(r, 4, lora_parts(f32)) : 0;
 }
 
 template <int kSteps, bool kF32, LoraMode kMode>
