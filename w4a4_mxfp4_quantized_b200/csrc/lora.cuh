@@ -112,6 +112,9 @@ __device__ __forceinline__ uint4 lora_ld(const uint16_t *p, bool on) {
     return on ? __ldg(reinterpret_cast<const uint4 *>(p)) : make_uint4(0u, 0u, 0u, 0u);
 }
 
+// Chunks of up to `most` rows; rows < 2^31, so nothing is added to them.
+__host__ __device__ constexpr int32_t lora_chunk_count(int32_t rows, int32_t most) { return rows / most + (rows % most != 0); }
+
 struct LoraChunk {
     int32_t a, rows;   // adapter (L: rows of no adapter), rows; rows = 0: there is no such chunk
     int64_t row0;
@@ -131,7 +134,7 @@ __device__ __forceinline__ LoraChunk lora_find_chunk(const LoraArgs &p, int z, i
     for (int base = 0; base <= p.L; base += 32) {
         const int g = base + lane;
         const int32_t lo = g <= p.L ? s_off[g] : 0, rows = g <= p.L ? max(s_off[g + 1] - lo, 0) : 0;
-        const int32_t n = (rows + most - 1) / most;
+        const int32_t n = lora_chunk_count(rows, most);
         int32_t x = n;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
