@@ -55,7 +55,7 @@ struct LoraArgs {
     const int32_t *offsets;   // [L + 1]
     const int32_t *row_index; // [M] or nullptr: rows are sorted already
     int64_t ldy, ldo, ldx, M, N, K;
-    int32_t r, L, f32;
+    int32_t r, L;
     uint16_t *v;              // workspace (two launches): V per chunk, [part][row][stride]
     int32_t slices;           // of the columns, per chunk
 };

@@ -1308,7 +1308,6 @@ macaq_status lora_add(const LoraArgs &p, int32_t dtype, void *workspace, size_t 
     macaq_status s = device_info(&dev);
     if (s != MACAQ_OK) return s;
     LoraArgs g = p;
-    g.f32 = f32;
     g.v = static_cast<uint16_t *>(workspace);
     auto run = [&](auto f) {
         constexpr bool kF32 = decltype(f)::value;
