@@ -99,3 +99,69 @@ def test_sorted_rows_without_an_index(M, r, dtype):
     mq.lora_add(Y, X, c["A"], c["B"], off, scale=c["scale"])
     torch.cuda.synchronize()
     assert torch.equal(out, want) and torch.equal(Y, want)
+
+
+def among(c, L, seed):
+    """The same call with its adapters somewhere in a bank of L, whose others are NaN: they must not be read."""
+    g = torch.Generator("cuda").manual_seed(seed)
+    where = torch.sort(torch.randperm(L, generator=g, device="cuda")[:c["L"]]).values
+    bank = {k: torch.full((L, *c[k].shape[1:]), float("nan"), dtype=c[k].dtype, device="cuda") for k in ("A", "B", "scale")}
+    for k in bank:
+        bank[k][where] = c[k]
+    ids = torch.where(c["ids"] < c["L"], where[c["ids"].clamp(max=c["L"] - 1).long()], -1).to(torch.int32)
+    return dict(c, **bank, ids=ids, L=L)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,r,L", [(1, 16, 64), (40, 16, 1024), (40, 128, 65), (300, 40, 1024), (300, 104, 200), (1500, 40, 64),
+                                   (1500, 16, 64), (1500, 128, 1000), (700, 72, 64), (5000, 8, 1024)])
+def test_few_adapters_of_a_large_bank(M, r, L, dtype):
+    c = among(make(M + r, M, 200, 328, r, 4, dtype), L, r)
+    off, row, _ = mq.row_groups(c["ids"], L)
+    o = Guarded(c["Y"].numel() * c["Y"].element_size(), dtype=dtype, shape=c["Y"].shape)
+    need = mq.lora_workspace_bytes(M, r, L, mq.OUT_F32 if dtype == torch.float32 else mq.OUT_BF16, 200, 328)
+    ws = Guarded(need) if need > 0 else None
+    mq.lora_add(c["Y"], c["X"], c["A"], c["B"], off, row, scale=c["scale"], out=o.t, workspace=ws and ws.t)
+    torch.cuda.synchronize()
+    assert o.intact() and (ws is None or ws.intact()) and torch.equal(o.t, c["want"])
+    mq.lora_add(c["Y"], c["X"], c["A"], c["B"], off, row, scale=c["scale"])   # in place
+    torch.cuda.synchronize()
+    assert torch.equal(c["Y"], c["want"])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,L,N", [(64, 64, 328), (500, 100, 4104), (1100, 64, 328), (1100, 64, 4104), (3000, 1024, 328), (3000, 70, 4104)])
+def test_every_adapter_of_a_large_bank(M, L, N, dtype):
+    """A handful of rows to nearly every adapter: more chunks than a round of the device, and rows of none."""
+    c = make(M + L, M, 72, N, 40, L, dtype)
+    off, row, _ = mq.row_groups(c["ids"], L)
+    out = mq.lora_add(c["Y"], c["X"], c["A"], c["B"], off, row, scale=c["scale"], out=torch.empty_like(c["Y"]))
+    mq.lora_add(c["Y"], c["X"], c["A"], c["B"], off, row, scale=c["scale"])
+    torch.cuda.synchronize()
+    assert torch.equal(out, c["want"]) and torch.equal(c["Y"], c["want"])
+
+
+@pytest.mark.parametrize("M", [40, 2000])
+def test_no_row_of_a_large_bank_has_an_adapter(M):
+    c = make(1, M, 72, 264, 40, 100, torch.bfloat16, absent=1.1)
+    off, row, _ = mq.row_groups(c["ids"], 100)
+    out = mq.lora_add(c["Y"], c["X"], c["A"], c["B"], off, row, out=torch.empty_like(c["Y"]))
+    before = c["Y"].clone()
+    mq.lora_add(c["Y"], c["X"], c["A"], c["B"], off, row)
+    torch.cuda.synchronize()
+    assert torch.equal(out, before) and torch.equal(c["Y"], before)
+
+
+@pytest.mark.parametrize("M", [90, 2000])
+def test_malformed_plans_of_a_large_bank_stay_inside_the_buffers(M):
+    """Offsets that go back and forth or leave the rows: more chunks than a sound plan can have, in both launch forms."""
+    L, K, N, r = 100, 72, 264, 40
+    c = make(2, M, K, N, r, L, torch.bfloat16)
+    big = 2 ** 31 - 1
+    for off in ([0, M] * (L // 2) + [0], [0, big, -5, M // 2] * 25 + [7], [big] * (L + 1), [-1] * (L + 1)):
+        o = Guarded(M * N * 2, dtype=torch.bfloat16, shape=(M, N))
+        need = mq.lora_workspace_bytes(M, r, L, mq.OUT_BF16, K, N)
+        ws = Guarded(need) if need > 0 else None
+        mq.lora_add(c["Y"], c["X"], c["A"], c["B"], torch.tensor(off, dtype=torch.int32, device="cuda"), out=o.t, workspace=ws and ws.t)
+        torch.cuda.synchronize()
+        assert o.intact() and (ws is None or ws.intact())

@@ -57,7 +57,9 @@ struct LoraArgs {
     int64_t ldy, ldo, ldx, M, N, K;
     int32_t r, L;
     uint16_t *v;              // workspace (two launches): V per chunk, [part][row][stride]
-    int32_t slices;           // of the columns, per chunk
+    int32_t slices;           // CTAs per chunk, each with its slice of the columns; 0: by the number of chunks that there are
+    int32_t chunks;           // the most that a sound plan has
+    int32_t room;             // CTAs of one round
 };
 
 // Shared memory for rank r, chunks of 16 mt rows and `parts` bf16 parts of V: the CTA's partial V per k split, its sum, the
@@ -156,6 +158,56 @@ __device__ __forceinline__ LoraChunk lora_find_chunk(const LoraArgs &p, int z, i
     return ch;
 }
 
+// The numbers of all groups' first chunks: first[g], and of all chunks first[L + 1]. Thread i has the groups from i * per on.
+// s_sum: one entry per warp.
+__device__ __forceinline__ void lora_scan_chunks(const LoraArgs &p, int most, int32_t *first, int64_t *s_sum) {
+    constexpr int kPer = (kRouteMaxExperts + 1 + kLoraThreads - 1) / kLoraThreads;
+    constexpr int64_t kTop = (int64_t{1} << 31) - 1;   // of a plan that lists rows many times
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per = (p.L + kLoraThreads) / kLoraThreads, g0 = threadIdx.x * per;
+    int32_t off[kPer + 1], n[kPer];
+#pragma unroll
+    for (int i = 0; i <= kPer; ++i)
+        off[i] = g0 + i > p.L ? static_cast<int32_t>(p.M)
+                              : static_cast<int32_t>(min(max(static_cast<int64_t>(__ldcg(p.offsets + g0 + i)), int64_t{0}), p.M));
+    int64_t sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        n[i] = i < per && g0 + i <= p.L ? lora_chunk_count(max(off[i + 1] - off[i], 0), most) : 0;
+        sum += n[i];
+    }
+    int64_t x = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+    }
+    if (lane == 31) s_sum[warp] = x;
+    __syncthreads();
+    int64_t at = x - sum;
+    for (int w = 0; w < warp; ++w) at += s_sum[w];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        if (i >= per || g0 + i > p.L) break;
+        first[g0 + i] = static_cast<int32_t>(min(at, kTop));
+        at += n[i];
+        if (g0 + i == p.L) first[p.L + 1] = static_cast<int32_t>(min(at, kTop));
+    }
+    __syncthreads();
+}
+
+// Chunk z from those numbers.
+__device__ __forceinline__ LoraChunk lora_chunk_at(const LoraArgs &p, int z, int most, const int32_t *first) {
+    int a = 0;   // the last group whose first chunk is not after z
+    for (int end = p.L + 1; end - a > 1;) {
+        const int mid = (a + end) / 2;
+        if (first[mid] <= z) a = mid;
+        else end = mid;
+    }
+    auto offset = [&](int i) { return i > p.L ? p.M : min(max(static_cast<int64_t>(__ldcg(p.offsets + i)), int64_t{0}), p.M); };
+    const int64_t lo = offset(a), skip = static_cast<int64_t>(z - first[a]) * most;
+    return {a, static_cast<int32_t>(min(max(offset(a + 1) - lo - skip, int64_t{0}), static_cast<int64_t>(most))), lo + skip};
+}
+
 // Eight neighbouring outputs of a row: out = y + d.
 template <bool kF32>
 struct LoraPiece {
@@ -191,7 +243,10 @@ struct LoraPiece {
     }
 };
 
-// Grid: `slices` CTAs per chunk: clusters of eight (kFused), one cluster of 1 to 8 (kShrink), without clusters (kExpand). kSteps: 32-wide steps of the rank.
+// Grid: `slices` CTAs per chunk: clusters of eight (kFused), one cluster of 1 to 8 (kShrink), without clusters (kExpand).
+// slices = 0, for calls whose adapters may mostly have no rows: a CTA for every chunk that there can be, and for one round at
+// least, in clusters of eight; the device counts the chunks and gives each as many neighbouring CTAs as that leaves, up to a
+// cluster's eight (then whole clusters) for V. kSteps: 32-wide steps of the rank.
 template <int kSteps, bool kF32, LoraMode kMode>
 __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
     constexpr int kMt = lora_tiles(kMode);   // m16 tiles of a chunk
@@ -206,16 +261,42 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
     if constexpr (kMode != kExpand) griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int cluster = kMode == kShrink ? p.slices : kLoraCluster, log2_cluster = 31 - __clz(cluster);   // a power of two
-    const int rank = blockIdx.x & (cluster - 1), z = blockIdx.x / p.slices, slice = blockIdx.x % p.slices;
-    const LoraChunk ch = lora_find_chunk(p, z, kRows, s_off);
-    if (ch.rows == 0 || (ch.a == p.L && (kMode == kShrink || p.out == p.y))) {   // the same for the whole cluster
-        if constexpr (kMode == kExpand) griddep_wait();
+    int cluster = kMode == kFused ? kLoraCluster : p.slices;   // CTAs that make a chunk's V: a power of two
+    int slices = p.slices, rank, first_rank = 0, z, slice;
+    LoraChunk ch{0, 0, 0};
+    if (slices > 0) {
+        rank = blockIdx.x & (cluster - 1), z = blockIdx.x / slices, slice = blockIdx.x % slices;
+        ch = lora_find_chunk(p, z, kRows, s_off);
+    } else {
+        __shared__ int64_t s_sum[kLoraWarps];
+        lora_scan_chunks(p, kRows, s_off, s_sum);
+        const int steps = static_cast<int>((p.N + 31) / 32);
+        const int chunks = min(s_off[kMode == kShrink || p.out == p.y ? p.L : p.L + 1], p.chunks);   // rows of no adapter: copied
+        cluster = kMode == kExpand ? 1 : kLoraCluster;
+        while (cluster > 1 && chunks > p.room / cluster) cluster /= 2;
+        const int share = kMode == kShrink ? 1 : max(1, min(p.room / (cluster * max(chunks, 1)), steps / (kLoraWarps * cluster)));
+        slices = share * cluster;
+        rank = blockIdx.x & (cluster - 1), z = blockIdx.x / slices, slice = blockIdx.x % slices;
+        first_rank = (blockIdx.x & (kLoraCluster - 1)) - rank;
+        if (z < chunks) ch = lora_chunk_at(p, z, kRows, s_off);
+    }
+    // A CTA without work: the same for all of a chunk's CTAs, but others of the cluster may have some (slices = 0)
+    auto leave = [&]() {
+        if constexpr (kMode == kExpand) {
+            griddep_wait();
+        } else if (p.slices == 0) {
+            cluster_sync();
+            cluster_sync();
+        }
+    };
+    if (ch.rows == 0 || (ch.a == p.L && (kMode == kShrink || p.out == p.y))) {
+        leave();
         return;
     }
+    const int log2_cluster = 31 - __clz(cluster);
     const int r = p.r;
     // this CTA's columns, in steps of 32, and k, in steps of 32 or 64
-    const int64_t nsteps = (p.N + 31) / 32, n_begin = nsteps * slice / p.slices, n_end = nsteps * (slice + 1) / p.slices;
+    const int64_t nsteps = (p.N + 31) / 32, n_begin = nsteps * slice / slices, n_end = nsteps * (slice + 1) / slices;
     constexpr int kWide = kMode == kShrink ? 64 : 32;
     const int64_t ksteps = (p.K + kWide - 1) / kWide, k_begin = ksteps * rank >> log2_cluster, k_end = ksteps * (rank + 1) >> log2_cluster;
     for (int i = threadIdx.x; i < kRows; i += kLoraThreads) {
@@ -229,7 +310,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
     __syncthreads();
 
     if (ch.a == p.L) {   // rows of no adapter
-        if constexpr (kMode == kExpand) griddep_wait();   // out may still be in use
+        leave();         // kExpand: out may still be in use
         // a warp per row, eight pieces of it in flight
         constexpr int kAhead = 8;
         const int64_t stop = min(n_end * 32, p.N);
@@ -447,7 +528,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
                 if (c >= cluster) continue;
                 asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
                              : "=f"(a0[c]), "=f"(a1[c])
-                             : "r"(map_to_rank(smem_u32(mine + 2 * i), c))
+                             : "r"(map_to_rank(smem_u32(mine + 2 * i), first_rank + c))
                              : "memory");
             }
 #pragma unroll

@@ -1223,16 +1223,22 @@ macaq_status moe_w4a16(const MoeArgs &a, void *workspace, size_t ws_bytes, cudaS
 }
 
 // ------------------------------------------------------------------------ low-rank adapters
+constexpr int32_t kLoraManyAdapters = 33;         // from which on the device counts the chunks and shares them out
 constexpr int64_t kLoraRounds = 74;             // 16-row chunks of two rounds of clusters of eight (two CTAs per SM)
 constexpr int64_t kLoraNarrowWork = 12000000;   // 16-row chunks times entries of an adapter's A and B
+constexpr int64_t kLoraBankWork = 8000000;        // many: M / 16 x entries of an adapter's A and B, from which on they are
 
 // How a call is cut. In 16-row chunks (one launch) A and B are read and multiplied for every 16 rows, in 64-row chunks (two
-// launches) a quarter as often, where adapters have the rows to fill them. bf16, 4 adapters, in 16-row against 64-row chunks:
+// launches) a quarter as often. Measured on B200 in 16-row against 64-row chunks, us in a graph:
+// Few adapters (L < 33): where they have the rows to fill them. bf16, 4 adapters, in 16-row against 64-row chunks:
 // 4096 -> 14336, rank 64, 64 rows (11 M) 13.0 against 10.6 us, 128 rows (15 M) 16.2 against 11.2, 256 rows 22.7 against 16.3;
 // 4096 -> 1024, rank 64, 512 rows (12 M) 11.8 against 11.7 us, rank 128, 256 rows (14 M) 19.1 against 13.9; 1000 rows of 16
 // adapters of rank 16 (80 chunks) 15.8 against 13.0 us. Two launches take 16 us of the host's time from Python, one 10, so
 // that calls under some 14 us stay with one. With 16 rows per adapter rank 16 is faster in 16-row chunks (512 rows on
 // 1024 columns 11.6 against 12.8 us, fp32 12.2 against 15.0), rank 64 in 64-row chunks (19.1 against 17.2, 25.8 against 18.9).
+// Many adapters, which may mostly have no rows: only the product's size goes into the rule. 4096 -> 14336, rank 16, 256 rows of 4
+// active adapters 16.9 against 17.5, 512 rows 25.1 against 19.9, of 64 30.7 against 32.1; rank 64, 512 rows of 4 36.9 against 24.3, of 64 45.8 against 51.7, of 256 126 against 148; 2048 rows of 4 121 against 51, of 1024 546 against 478;
+// 4096 -> 1024, rank 16, 1024 rows of 4 12.0 against 13.2, of 64 12.3 against 19.6.
 struct LoraPlan {
     bool wide;
     int64_t chunks;
@@ -1244,7 +1250,11 @@ int64_t lora_chunks(int64_t M, int32_t L, int rows) { return std::min<int64_t>(L
 LoraPlan lora_plan(int64_t M, int32_t L, int32_t r, int64_t K, int64_t N) {
     const int64_t narrow = lora_chunks(M, L, 16);
     LoraPlan p;
-    p.wide = M >= (r > 32 ? 16 : 32) * static_cast<int64_t>(L) && (narrow > kLoraRounds || narrow * r * (K + N) > kLoraNarrowWork);
+    if (L >= kLoraManyAdapters) {
+        p.wide = M / 16 * r * (K + N) > kLoraBankWork;
+    } else {
+        p.wide = M >= (r > 32 ? 16 : 32) * static_cast<int64_t>(L) && (narrow > kLoraRounds || narrow * r * (K + N) > kLoraNarrowWork);
+    }
     p.chunks = p.wide ? lora_chunks(M, L, 64) : narrow;
     return p;
 }
@@ -1254,34 +1264,44 @@ size_t lora_workspace_bytes(const LoraPlan &p, int32_t r, bool f32) {
 }
 
 template <int kSteps, bool kF32, LoraMode kMode>
-macaq_status launch_lora(LoraArgs g, int64_t chunks, int64_t slices, cudaStream_t st) {
+macaq_status launch_lora(LoraArgs g, int64_t ctas, int64_t slices, int64_t cluster, cudaStream_t st) {
     auto k = lora_add_kernel<kSteps, kF32, kMode>;
     const size_t smem = lora_smem_bytes(g.r, kSteps, kF32, kMode);
     macaq_status s = set_smem(k, smem);
     if (s != MACAQ_OK) return s;
     g.slices = static_cast<int32_t>(slices);
-    if (chunks * slices >= (int64_t(1) << 31)) return MACAQ_ERR_SHAPE;
-    return launch(k, dim3(static_cast<unsigned>(chunks * slices)), dim3(kLoraThreads), smem, st,
-                  kMode == kExpand ? 1 : (kMode == kShrink ? static_cast<int>(slices) : kLoraCluster), g);
+    if (ctas >= (int64_t(1) << 31)) return MACAQ_ERR_SHAPE;
+    return launch(k, dim3(static_cast<unsigned>(ctas)), dim3(kLoraThreads), smem, st, static_cast<int>(cluster), g);
 }
 
 template <int kSteps, bool kF32>
-macaq_status run_lora(const LoraArgs &g, const LoraPlan &p, int sms, cudaStream_t st) {
-    const int64_t nsteps = (g.N + 31) / 32;
-    if (p.wide) {
-        // K is split as far as one round of two CTAs per SM goes
-        int64_t split = kLoraCluster;
-        while (split > 1 && p.chunks * split > 2 * sms) split /= 2;
-        const macaq_status s = launch_lora<kSteps, kF32, kShrink>(g, p.chunks, split, st);
+macaq_status run_lora(LoraArgs g, const LoraPlan &p, int sms, cudaStream_t st) {
+    const int64_t nsteps = (g.N + 31) / 32, room = 2 * sms;   // CTAs of one round: two per SM
+    g.chunks = static_cast<int32_t>(p.chunks);
+    if (g.L >= kLoraManyAdapters) {
+        auto ctas = [&](int64_t room) { return (std::max(p.chunks, room) + kLoraCluster - 1) / kLoraCluster * kLoraCluster; };
+        if (!p.wide) {
+            g.room = static_cast<int32_t>(room * 7 / 8);   // whole clusters: each has all its SMs in one GPC
+            return launch_lora<kSteps, kF32, kFused>(g, ctas(g.room), 0, kLoraCluster, st);
+        }
+        g.room = static_cast<int32_t>(room);
+        const macaq_status s = launch_lora<kSteps, kF32, kShrink>(g, ctas(g.room), 0, kLoraCluster, st);
         if (s != MACAQ_OK) return s;
-        // slices of at least one step per warp, for one round of two CTAs per SM (what comes before a CTA's first step, about
-        // 5 us, is paid once)
-        const int64_t slices = std::max<int64_t>(1, std::min<int64_t>(nsteps / kLoraWarps, 2 * sms / p.chunks));
-        return launch_lora<kSteps, kF32, kExpand>(g, p.chunks, slices, st);
+        return launch_lora<kSteps, kF32, kExpand>(g, ctas(g.room), 0, 1, st);
+    }
+    if (p.wide) {
+        // K is split as far as one round goes
+        int64_t split = kLoraCluster;
+        while (split > 1 && p.chunks * split > room) split /= 2;
+        const macaq_status s = launch_lora<kSteps, kF32, kShrink>(g, p.chunks * split, split, split, st);
+        if (s != MACAQ_OK) return s;
+        // slices of at least one step per warp, for one round (what comes before a CTA's first step, about 5 us, is paid once)
+        const int64_t slices = std::max<int64_t>(1, std::min<int64_t>(nsteps / kLoraWarps, room / p.chunks));
+        return launch_lora<kSteps, kF32, kExpand>(g, p.chunks * slices, slices, 1, st);
     }
     // clusters that share a chunk: while SMs are left, and every warp has a step
-    const int64_t share = std::max<int64_t>(1, std::min<int64_t>(2 * sms / (kLoraCluster * p.chunks), nsteps / (kLoraCluster * kLoraWarps)));
-    return launch_lora<kSteps, kF32, kFused>(g, p.chunks, share * kLoraCluster, st);
+    const int64_t share = std::max<int64_t>(1, std::min<int64_t>(room / (kLoraCluster * p.chunks), nsteps / (kLoraCluster * kLoraWarps)));
+    return launch_lora<kSteps, kF32, kFused>(g, p.chunks * share * kLoraCluster, share * kLoraCluster, kLoraCluster, st);
 }
 
 macaq_status lora_add(const LoraArgs &p, int32_t dtype, void *workspace, size_t ws_bytes, cudaStream_t st) {
@@ -1574,9 +1594,14 @@ macaq_status macaq_lora_add(const void *Y, int64_t ldy, void *out, int64_t ldo, 
 size_t macaq_lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int32_t r, int32_t L, int32_t dtype) {
     if (M <= 0 || M >= (int64_t(1) << 31) || L < 1 || L > macaq::kRouteMaxExperts || r < 8 || r > macaq::kLoraMaxRank || r % 8)
         return 0;
-    constexpr int64_t kMost = int64_t(1) << 24;
+    constexpr int64_t kLeast = 8, kMost = int64_t(1) << 24;
     if (K < 0 || K > kMost || N < 0 || N > kMost) return 0;
-    return macaq::lora_workspace_bytes(macaq::lora_plan(M, L, r, K == 0 ? kMost : K, N == 0 ? kMost : N), r, dtype == MACAQ_OUT_F32);
+    const bool f32 = dtype == MACAQ_OUT_F32;
+    size_t most = 0;   // a width that is not given may be any: the least and the largest take two launches first, by either rule
+    for (const int64_t k : {K == 0 ? kLeast : K, K == 0 ? kMost : K})
+        for (const int64_t n : {N == 0 ? kLeast : N, N == 0 ? kMost : N})
+            most = std::max(most, macaq::lora_workspace_bytes(macaq::lora_plan(M, L, r, k, n), r, f32));
+    return most;
 }
 
 }  // extern "C"
