@@ -1228,6 +1228,12 @@ constexpr int64_t kLoraRounds = 74;             // 16-row chunks of two rounds o
 constexpr int64_t kLoraNarrowWork = 12000000;   // 16-row chunks times entries of an adapter's A and B
 constexpr int64_t kLoraBankWork = 8000000;        // many: M / 16 x entries of an adapter's A and B, from which on they are
 
+// CTAs of one round: two per SM where their shared memory (static arrays and the system's KB with it) fits twice.
+int64_t lora_room(int32_t r, bool f32, LoraMode mode, int64_t sms) {
+    constexpr int kPerSm = 228 * 1024, kOther = 7 * 1024;
+    return 2 * (lora_smem_bytes(r, lora_padded_rank(r) / 32, f32, mode) + kOther) <= kPerSm ? 2 * sms : sms;
+}
+
 // How a call is cut. In 16-row chunks (one launch) A and B are read and multiplied for every 16 rows, in 64-row chunks (two
 // launches) a quarter as often. Measured on B200 in 16-row against 64-row chunks, us in a graph:
 // Few adapters (L < 33): where they have the rows to fill them. bf16, 4 adapters, in 16-row against 64-row chunks:
@@ -1276,31 +1282,37 @@ macaq_status launch_lora(LoraArgs g, int64_t ctas, int64_t slices, int64_t clust
 
 template <int kSteps, bool kF32>
 macaq_status run_lora(LoraArgs g, const LoraPlan &p, int sms, cudaStream_t st) {
-    const int64_t nsteps = (g.N + 31) / 32, room = 2 * sms;   // CTAs of one round: two per SM
+    const int64_t nsteps = (g.N + 31) / 32;
+    const int64_t fused = lora_room(g.r, kF32, kFused, sms), shrink = lora_room(g.r, kF32, kShrink, sms),
+                  expand = lora_room(g.r, kF32, kExpand, sms);
     g.chunks = static_cast<int32_t>(p.chunks);
     if (g.L >= kLoraManyAdapters) {
         auto ctas = [&](int64_t room) { return (std::max(p.chunks, room) + kLoraCluster - 1) / kLoraCluster * kLoraCluster; };
         if (!p.wide) {
-            g.room = static_cast<int32_t>(room * 7 / 8);   // whole clusters: each has all its SMs in one GPC
+            g.room = static_cast<int32_t>(fused * 7 / 8);   // whole clusters: each has all its SMs in one GPC
             return launch_lora<kSteps, kF32, kFused>(g, ctas(g.room), 0, kLoraCluster, st);
         }
-        g.room = static_cast<int32_t>(room);
+        g.room = static_cast<int32_t>(shrink);
         const macaq_status s = launch_lora<kSteps, kF32, kShrink>(g, ctas(g.room), 0, kLoraCluster, st);
         if (s != MACAQ_OK) return s;
+        g.room = static_cast<int32_t>(expand);
         return launch_lora<kSteps, kF32, kExpand>(g, ctas(g.room), 0, 1, st);
     }
     if (p.wide) {
         // K is split as far as one round goes
         int64_t split = kLoraCluster;
-        while (split > 1 && p.chunks * split > room) split /= 2;
+        while (split > 1 && p.chunks * split > shrink) split /= 2;
         const macaq_status s = launch_lora<kSteps, kF32, kShrink>(g, p.chunks * split, split, split, st);
         if (s != MACAQ_OK) return s;
-        // slices of at least one step per warp, for one round (what comes before a CTA's first step, about 5 us, is paid once)
+        // Slices of at least one step per warp, for one round (what comes before a CTA's first step, about 5 us, is paid once). Where
+        // a third of the chunks may not be there, for two CTAs per SM even if one fits (fp32): 256 rows of 4 adapters of rank
+        // 32 on 4096 -> 14336 17.1 us, for one 20.8; 2048 rows 78.3 against 77.5, of rank 64 92.7 against 88.7.
+        const int64_t room = g.M / 64 >= 2 * (static_cast<int64_t>(g.L) + 1) ? expand : 2 * static_cast<int64_t>(sms);
         const int64_t slices = std::max<int64_t>(1, std::min<int64_t>(nsteps / kLoraWarps, room / p.chunks));
         return launch_lora<kSteps, kF32, kExpand>(g, p.chunks * slices, slices, 1, st);
     }
     // clusters that share a chunk: while SMs are left, and every warp has a step
-    const int64_t share = std::max<int64_t>(1, std::min<int64_t>(room / (kLoraCluster * p.chunks), nsteps / (kLoraCluster * kLoraWarps)));
+    const int64_t share = std::max<int64_t>(1, std::min<int64_t>(fused / (kLoraCluster * p.chunks), nsteps / (kLoraCluster * kLoraWarps)));
     return launch_lora<kSteps, kF32, kFused>(g, p.chunks * share * kLoraCluster, share * kLoraCluster, kLoraCluster, st);
 }
 
