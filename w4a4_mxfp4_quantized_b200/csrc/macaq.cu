@@ -1224,8 +1224,7 @@ macaq_status moe_w4a16(const MoeArgs &a, void *workspace, size_t ws_bytes, cudaS
 
 // ------------------------------------------------------------------------ low-rank adapters
 constexpr int32_t kLoraManyAdapters = 33;         // from which on the device counts the chunks and shares them out
-constexpr int64_t kLoraRounds = 74;             // 16-row chunks of two rounds of clusters of eight (two CTAs per SM)
-constexpr int64_t kLoraNarrowWork = 12000000;   // 16-row chunks times entries of an adapter's A and B
+constexpr int64_t kLoraColumnWork = 900;          // few adapters: chunks x rank x N / K, from which on two launches are faster
 constexpr int64_t kLoraBankWork = 8000000;        // many: M / 16 x entries of an adapter's A and B, from which on they are
 
 // CTAs of one round: two per SM where their shared memory (static arrays and the system's KB with it) fits twice.
@@ -1236,14 +1235,18 @@ int64_t lora_room(int32_t r, bool f32, LoraMode mode, int64_t sms) {
 
 // How a call is cut. In 16-row chunks (one launch) A and B are read and multiplied for every 16 rows, in 64-row chunks (two
 // launches) a quarter as often. Measured on B200 in 16-row against 64-row chunks, us in a graph:
-// Few adapters (L < 33): where they have the rows to fill them. bf16, 4 adapters, in 16-row against 64-row chunks:
-// 4096 -> 14336, rank 64, 64 rows (11 M) 13.0 against 10.6 us, 128 rows (15 M) 16.2 against 11.2, 256 rows 22.7 against 16.3;
-// 4096 -> 1024, rank 64, 512 rows (12 M) 11.8 against 11.7 us, rank 128, 256 rows (14 M) 19.1 against 13.9; 1000 rows of 16
-// adapters of rank 16 (80 chunks) 15.8 against 13.0 us. Two launches take 16 us of the host's time from Python, one 10, so
-// that calls under some 14 us stay with one. With 16 rows per adapter rank 16 is faster in 16-row chunks (512 rows on
-// 1024 columns 11.6 against 12.8 us, fp32 12.2 against 15.0), rank 64 in 64-row chunks (19.1 against 17.2, 25.8 against 18.9).
-// Many adapters, which may mostly have no rows: only the product's size goes into the rule. 4096 -> 14336, rank 16, 256 rows of 4
-// active adapters 16.9 against 17.5, 512 rows 25.1 against 19.9, of 64 30.7 against 32.1; rank 64, 512 rows of 4 36.9 against 24.3, of 64 45.8 against 51.7, of 256 126 against 148; 2048 rows of 4 121 against 51, of 1024 546 against 478;
+// Few adapters (L < 33, a chunk per adapter as good as certain): 64-row chunks need rows to fill them, 16 per adapter (256
+// rows of 32 adapters, 4096 -> 14336, rank 16 18.6 against 20.4, rank 64 27.4 against 30.2; 512 rows 30.1 against 24.9, 46.3
+// against 39.5). Then they win where the 16-row chunks are more than the clusters of one round (4096 -> 1024, rank 64, one
+// adapter, 256 rows 10.1 against 11.3, 1024 rows 25.5 against 14.7), or where the columns outweigh the second launch, whose
+// V waits for K: 4096 -> 14336, rank 64, 16 rows 9.6 against 9.1, 64 rows 12.5 against 11.1, 256 rows 17.0 against 15.1;
+// rank 16, 64 rows 7.7 against 8.4, 256 rows 13.4 against 11.1; 4096 -> 4096, rank 64, 64 rows 8.7 against 10.8, 256 rows
+// 13.1 against 11.3; 14336 -> 4096, rank 64, 64 rows 11.8 against 19.3, 512 rows 19.1 against 25.8; 1024 -> 4096, rank 64,
+// 16 rows 7.7 against 7.4. For that ranks up to 32 need 32 rows per adapter (1024 -> 4096, rank 16, 256 rows of 16 adapters
+// 8.0 against 9.7).
+// Many adapters, which may mostly have no rows: only the product's size goes into the rule. 4096 -> 14336, rank 16, 256 rows
+// of 4 active adapters 16.9 against 17.5, 512 rows 25.1 against 19.9, of 64 30.7 against 32.1; rank 64, 512 rows of 4 36.9
+// against 24.3, of 64 45.8 against 51.7, of 256 126 against 148; 2048 rows of 4 121 against 51, of 1024 546 against 478;
 // 4096 -> 1024, rank 16, 1024 rows of 4 12.0 against 13.2, of 64 12.3 against 19.6.
 struct LoraPlan {
     bool wide;
@@ -1253,13 +1256,16 @@ struct LoraPlan {
 // One chunk per adapter with rows and one for the rows of none, one more per `rows` rows.
 int64_t lora_chunks(int64_t M, int32_t L, int rows) { return std::min<int64_t>(L + 1, M) + M / rows; }
 
-LoraPlan lora_plan(int64_t M, int32_t L, int32_t r, int64_t K, int64_t N) {
+LoraPlan lora_plan(int64_t M, int32_t L, int32_t r, int64_t K, int64_t N, bool f32) {
+    constexpr int64_t kSms = 148;   // the workspace's size is asked for without a device
     const int64_t narrow = lora_chunks(M, L, 16);
     LoraPlan p;
     if (L >= kLoraManyAdapters) {
         p.wide = M / 16 * r * (K + N) > kLoraBankWork;
     } else {
-        p.wide = M >= (r > 32 ? 16 : 32) * static_cast<int64_t>(L) && (narrow > kLoraRounds || narrow * r * (K + N) > kLoraNarrowWork);
+        const int64_t round = lora_room(r, f32, kFused, kSms) / kLoraCluster * 15 / 16;   // the last clusters find no whole GPC's share
+        p.wide = M >= 16 * static_cast<int64_t>(L) &&
+                 (narrow > round || (M >= (r > 32 ? 16 : 32) * static_cast<int64_t>(L) && narrow * r * N > kLoraColumnWork * K));
     }
     p.chunks = p.wide ? lora_chunks(M, L, 64) : narrow;
     return p;
@@ -1333,7 +1339,7 @@ macaq_status lora_add(const LoraArgs &p, int32_t dtype, void *workspace, size_t 
         !aligned16(p.row_index) || !aligned4(p.scale) || !aligned16(workspace))
         return MACAQ_ERR_ALIGNMENT;
     const bool f32 = dtype == MACAQ_OUT_F32;
-    const LoraPlan plan = lora_plan(p.M, p.L, p.r, p.K, p.N);
+    const LoraPlan plan = lora_plan(p.M, p.L, p.r, p.K, p.N, f32);
     const size_t need = lora_workspace_bytes(plan, p.r, f32);
     if (need > 0 && (workspace == nullptr || ws_bytes < need)) return MACAQ_ERR_WORKSPACE;
     DeviceInfo dev;
@@ -1612,7 +1618,7 @@ size_t macaq_lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int32_t r, in
     size_t most = 0;   // a width that is not given may be any: the least and the largest take two launches first, by either rule
     for (const int64_t k : {K == 0 ? kLeast : K, K == 0 ? kMost : K})
         for (const int64_t n : {N == 0 ? kLeast : N, N == 0 ? kMost : N})
-            most = std::max(most, macaq::lora_workspace_bytes(macaq::lora_plan(M, L, r, k, n), r, f32));
+            most = std::max(most, macaq::lora_workspace_bytes(macaq::lora_plan(M, L, r, k, n, f32), r, f32));
     return most;
 }
 
