@@ -200,11 +200,12 @@ __device__ __forceinline__ void moe_find_items(const MoeArgs &a, int c, int ctas
 }
 
 // log2 of the power of two s that a group is scaled by before fp16, from its largest magnitude: 0 when that is in
-// [2^-10, 2^15) or zero, else what brings it to the range's nearer end.
+// [2^-10, 2^15) or zero, else what brings it to the range's nearer end. A value below the normal numbers has no exponent to
+// go by: 2^126 brings it under 1, and its last bit, 2^-149, to 2^-23.
 __device__ __forceinline__ int moe_shift(float top) {
     const int e = static_cast<int>(__float_as_uint(top) >> 23);
-    const int shift = e < 117 ? 117 - e : (e > 141 ? 141 - e : 0);
-    return top == 0.0f ? 0 : min(shift, 112);
+    const int shift = e < 117 ? (e == 0 ? 126 : 117 - e) : (e > 141 ? 141 - e : 0);
+    return top == 0.0f ? 0 : shift;
 }
 
 __device__ __forceinline__ float moe_pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
