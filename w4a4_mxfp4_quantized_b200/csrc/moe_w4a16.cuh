@@ -234,13 +234,23 @@ __device__ __forceinline__ void moe_tile_mma(uint32_t codes, const uint32_t (&wo
         for (int n = 0; n < kNt; ++n) {
             const uint4 b = *reinterpret_cast<const uint4 *>(bcol[n] + tile * 256 + c * 64);
             float xa = 1.0f, xb = 1.0f;
-            if constexpr (kScaled) xa = x0[n][tile * 4 + c], xb = x1[n][tile * 4 + c];
+            bool beyond = false;   // a scale times 1 / s past fp32, whose sums may be in it all the same (codes of zero)
+            if constexpr (kScaled) {
+                xa = x0[n][tile * 4 + c], xb = x1[n][tile * 4 + c];
+                beyond = isinf(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])) * fmaxf(xa, xb));
+            }
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
                 float d[4];
                 mma_f16_zero(d, a[2 * m][0], a[2 * m + 1][0], a[2 * m][1], a[2 * m + 1][1], b.x, b.y);
                 mma_f16(d, a[2 * m][2], a[2 * m + 1][2], a[2 * m][3], a[2 * m + 1][3], b.z, b.w);
-                if constexpr (kScaled) {
+                if (kScaled && beyond) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float w = s[2 * m + k / 2], x = k % 2 ? xb : xa;
+                        acc[m][n][k] = w > 1.0f && x > 1.0f ? fmaf(d[k] * w, x, acc[m][n][k]) : fmaf(d[k], w * x, acc[m][n][k]);
+                    }
+                } else if constexpr (kScaled) {
                     acc[m][n][0] = fmaf(d[0], s[2 * m] * xa, acc[m][n][0]);
                     acc[m][n][1] = fmaf(d[1], s[2 * m] * xb, acc[m][n][1]);
                     acc[m][n][2] = fmaf(d[2], s[2 * m + 1] * xa, acc[m][n][2]);
