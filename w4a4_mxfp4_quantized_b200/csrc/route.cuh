@@ -32,8 +32,11 @@ constexpr int kRouteWarps = 8;          // tokens in flight per CTA of the top-k
 constexpr int kGroupThreads = 1024;
 constexpr int kGroupWarps = kGroupThreads / 32;
 constexpr int kGroupCluster = 8;
-constexpr int kGroupOneCta = 2048;       // entries that one CTA sorts
-constexpr int kGroupWide = 16384;        // entries from which the cluster has 16 CTAs
+// Entries that one CTA sorts, and up to which a cluster has 8 CTAs, not 16. Measured with 1, 8, 16 CTAs in a graph, us: of 128 groups 512
+// entries 4.4, 4.8, 5.1; 1024 5.1, 4.9, 5.1; 2048 6.2, 4.9, 5.1; 4096 8.5, 5.1, 5.3; 8192 13.6, 5.9, 5.7; 16,384 23.6, 6.9, 6.2;
+// 65,536 84, 14.5, 9.8. Of 1024 groups 1024 entries 6.7, 7.4, 9.5; 8192 16.9, 8.5, 9.9; 32,768 52.7, 12.8, 12.1.
+constexpr int kGroupOneCta = 1024;
+constexpr int kGroupWide = 8192;
 constexpr int kRouteFusedTokens = 256;   // tokens whose experts are chosen in the same launch: one per warp of a cluster
 
 struct RouteArgs {
