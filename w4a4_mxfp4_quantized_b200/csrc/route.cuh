@@ -13,9 +13,9 @@
 // row of group g, pos[i] the sorted row of entry i (-1 for an id outside [0, E)), row_index[r] the token
 // (entry / topk) of sorted row r; entries of no group follow the last group in their order.
 //
-// Bound by latency: a prefill's 65,536 entries are 0.8 MB. One CTA sorts up to 2,048 entries, a cluster of eight CTAs more
-// (their counts meet in distributed shared memory, so one launch and no workspace do); with up to 256 tokens the
-// same launch chooses the experts too, a warp per token.
+// Bound by latency: a prefill's 65,536 entries are 0.8 MB. One CTA sorts up to 1,024 entries, a cluster of eight up to 8,192 and one
+// of sixteen more (their counts meet in distributed shared memory, so one launch and no workspace do); with up to 256 tokens
+// the same launch chooses the experts too, a warp per token.
 // Measured on B200 (128 experts, top-8): one token 4.9 us, 64 tokens 6.1, 8192 tokens 15.5 us in two launches (5.5 for the
 // choice, 9.6 for the sort); the sort of 64 entries 3.4 us.
 #pragma once
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_topk_kernel(RouteArgs 
         route_token<kVpl>(a, t, lane);
 }
 
-// The lanes of `live` whose bucket equals this lane's,, by one vote per bit. For 65,536 entries of 128 groups
+// The lanes of `live` whose bucket equals this lane's, by one vote per bit. For 65,536 entries of 128 groups
 // on eight CTAs this took 15.0 us, match.any 18.4.
 __device__ __forceinline__ uint32_t group_peers(uint32_t live, int b, int bits) {
     uint32_t peers = live;
@@ -157,7 +157,7 @@ __device__ __forceinline__ uint32_t group_peers(uint32_t live, int b, int bits) 
 
 // The row plan, by one CTA or a cluster (`ctas`): CTA c owns a contiguous piece of the tokens, each of its warps a
 // contiguous piece of their entries. A warp walks its piece 32 entries at a time, and the lanes with the same group find
-// one another (match_any), so ranks follow the entries' order and nothing is atomic; an entry's rank among the
+// one another by votes, so ranks follow the entries' order and nothing is atomic; an entry's rank among the
 // warp's entries of its group waits in pos. Shared memory: counts [warps][E + 1] (bucket E: no group), the CTA's totals,
 // the buckets' first rows and the totals of all CTAs [E + 1]. kVpl > 0: choose the experts first (kVpl per lane).
 template <int kVpl>
