@@ -114,7 +114,8 @@ def among(c, L, seed):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("M,r,L", [(1, 16, 64), (40, 16, 1024), (40, 128, 65), (300, 40, 1024), (300, 104, 200), (1500, 40, 64),
-                                   (1500, 16, 64), (1500, 128, 1000), (700, 72, 64), (5000, 8, 1024)])
+                                   (1500, 16, 64), (1500, 128, 1000), (700, 72, 64), (5000, 8, 1024), (70, 24, 32),
+                                   (70, 24, 33), (1500, 24, 32), (1500, 24, 33)])
 def test_few_adapters_of_a_large_bank(M, r, L, dtype):
     c = among(make(M + r, M, 200, 328, r, 4, dtype), L, r)
     off, row, _ = mq.row_groups(c["ids"], L)
@@ -130,7 +131,7 @@ def test_few_adapters_of_a_large_bank(M, r, L, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("M,L,N", [(64, 64, 328), (500, 100, 4104), (1100, 64, 328), (1100, 64, 4104), (3000, 1024, 328), (3000, 70, 4104)])
+@pytest.mark.parametrize("M,L,N", [(64, 64, 328), (100, 33, 328), (1500, 33, 4104), (500, 100, 4104), (1100, 64, 328), (1100, 64, 4104), (3000, 1024, 328), (3000, 70, 4104)])
 def test_every_adapter_of_a_large_bank(M, L, N, dtype):
     """A handful of rows to nearly every adapter: more chunks than a round of the device, and rows of none."""
     c = make(M + L, M, 72, N, 40, L, dtype)

@@ -5,10 +5,10 @@
 //   h   = silu(g) u,  h' = h diag(1/s_down,e) H_b'
 //   out[t] = sum_j weights[t, j] * (h'_{pos[t, j]} dq(W'_down,e)^T)
 //
-// Bound by HBM: every active expert's codes and scales (17/32 byte a weight), and an expert has a handful of rows, so the two
-// products are streams of weights against a small operand that stays in shared memory. They are read once per chunk of an expert's
-// rows: once in all up to 8 (16) rows, as long as panels of so many rows fit: K and I up to 6,144 (2,560). Wider layers have
-// smaller chunks (I = 14336: 2 rows), and experts with more rows than that stream their weights several times.
+// Bound by HBM: every active expert's codes and scales (17/32 byte a weight), and an expert has a handful of rows, so the
+// two products are streams of weights against a small operand that stays in shared memory. They are read once per chunk of
+// an expert's rows: once in all up to 8 (16) rows, as long as panels of so many rows fit: K and I up to 6,144 (2,560). Wider
+// layers have smaller chunks (I = 14336: 2 rows), and experts with more rows than that stream their weights several times.
 //
 // Plan. Three launches: gate, up and SwiGLU (kernel 1); down (kernel 2); the weighted sum of each token's choices (for few
 // rows one kernel does the last two, see moe_down_sum_kernel). The rows of an expert are cut into chunks of up to 8 or 16 (8
@@ -34,10 +34,11 @@
 // Measured on B200 (128 experts, top-8, 2048 x 768; a graph that cycles three layers): one token 15.7 us (20.2 MB), 8 tokens
 // 35.5 us (130 MB), 64 tokens 72.2 us (318 MB, 4.4 TB/s). With 64 tokens the two weight streams themselves run at 5.9 and
 // 5.8 TB/s (36 and 18 us) of the 6.5 that a copy reaches; the rest is three starts (plan 1.3 us, first loads and panel 3 to
-// 5 us, a launch's end to the next one's first instruction 1 to 1.5 us) and the closing of cut items (1 us). One token
-// is made of those latencies alone. Wider layers (top-8 of 128, 4096 x 1536): one token 29.7 us (80 MB), 8 tokens 110 us (541 MB), 64
-// tokens 261 us (1273 MB, 4.9 TB/s); top-8 of 256, 7168 x 2048: 50.8 (187 MB), 253 (1310 MB), 1010 us (5147 MB); top-2 of 8, 4096 x
-// 14336: 47.3 (187 MB), 150 (749 MB), and 64 tokens, whose experts have 16 rows in chunks of 2, 720 us (749 MB).
+// 5 us, a launch's end to the next one's first instruction 1 to 1.5 us) and the closing of cut items (1 us). One token is
+// made of those latencies alone. Wider layers (top-8 of 128, 4096 x 1536): one token 29.7 us (80 MB), 8 tokens 110 us (541
+// MB), 64 tokens 261 us (1273 MB, 4.9 TB/s); top-8 of 256, 7168 x 2048: 50.8 (187 MB), 253 (1310 MB), 1010 us (5147 MB);
+// top-2 of 8, 4096 x 14336: 47.3 (187 MB), 150 (749 MB), and 64 tokens, whose experts have 16 rows in chunks of 2, 720 us
+// (749 MB).
 // Sources: glonce.com page on MACaQ, paragraph 3 (weight-only serving) and paragraph 5 (grouped matmul);
 // aipolix.com page, paragraph 2 (the transform at the input of every linear).
 #pragma once

@@ -13,9 +13,9 @@
 // row of group g, pos[i] the sorted row of entry i (-1 for an id outside [0, E)), row_index[r] the token
 // (entry / topk) of sorted row r; entries of no group follow the last group in their order.
 //
-// Bound by latency: a prefill's 65,536 entries are 0.8 MB. One CTA sorts up to 1,024 entries, a cluster of eight up to 8,192 and one
-// of sixteen more (their counts meet in distributed shared memory, so one launch and no workspace do); with up to 256 tokens
-// the same launch chooses the experts too, a warp per token.
+// Bound by latency: a prefill's 65,536 entries are 0.8 MB. One CTA sorts up to 1,024 entries, a cluster of eight up to 8,192
+// and one of sixteen more (their counts meet in distributed shared memory, so one launch and no workspace do); with up to
+// 256 tokens the same launch chooses the experts too, a warp per token.
 // Measured on B200 (128 experts, top-8): one token 4.9 us, 64 tokens 6.1, 8192 tokens 15.5 us in two launches (5.5 for the
 // choice, 9.6 for the sort); the sort of 64 entries 3.4 us.
 #pragma once
@@ -32,9 +32,10 @@ constexpr int kRouteWarps = 8;          // tokens in flight per CTA of the top-k
 constexpr int kGroupThreads = 1024;
 constexpr int kGroupWarps = kGroupThreads / 32;
 constexpr int kGroupCluster = 8;
-// Entries that one CTA sorts, and up to which a cluster has 8 CTAs, not 16. Measured with 1, 8, 16 CTAs in a graph, us: of 128 groups 512
-// entries 4.4, 4.8, 5.1; 1024 5.1, 4.9, 5.1; 2048 6.2, 4.9, 5.1; 4096 8.5, 5.1, 5.3; 8192 13.6, 5.9, 5.7; 16,384 23.6, 6.9, 6.2;
-// 65,536 84, 14.5, 9.8. Of 1024 groups 1024 entries 6.7, 7.4, 9.5; 8192 16.9, 8.5, 9.9; 32,768 52.7, 12.8, 12.1.
+// Entries that one CTA sorts, and up to which a cluster has 8 CTAs, not 16. Measured with 1, 8, 16 CTAs in a graph, us: of
+// 128 groups 512 entries 4.4, 4.8, 5.1; 1024 5.1, 4.9, 5.1; 2048 6.2, 4.9, 5.1; 4096 8.5, 5.1, 5.3; 8192 13.6, 5.9, 5.7;
+// 16,384 23.6, 6.9, 6.2; 65,536 84, 14.5, 9.8. Of 1024 groups 1024 entries 6.7, 7.4, 9.5; 8192 16.9, 8.5, 9.9; 32,768 52.7,
+// 12.8, 12.1.
 constexpr int kGroupOneCta = 1024;
 constexpr int kGroupWide = 8192;
 constexpr int kRouteFusedTokens = 256;   // tokens whose experts are chosen in the same launch: one per warp of a cluster
