@@ -166,3 +166,36 @@ def test_malformed_plans_of_a_large_bank_stay_inside_the_buffers(M):
         mq.lora_add(c["Y"], c["X"], c["A"], c["B"], torch.tensor(off, dtype=torch.int32, device="cuda"), out=o.t, workspace=ws and ws.t)
         torch.cuda.synchronize()
         assert o.intact() and (ws is None or ws.intact())
+
+
+@pytest.mark.parametrize("M,r,L", [(40, 16, 4), (40, 16, 100), (1500, 40, 4), (1500, 40, 100)])
+def test_captured_once_and_replayed_with_other_plans(M, r, L):
+    """Router and adapters in one graph, two of them at once on two streams: the next replay has other adapters for the rows."""
+    runs = []
+    for seed in (1, 2):
+        first, second = (among(make(10 * seed + k, M, 136, 328, r, 4, torch.bfloat16), L, 7) for k in (0, 1))
+        Y, X, ids, A, B, scale = (first[k].clone() for k in ("Y", "X", "ids", "A", "B", "scale"))
+
+        def step():
+            off, row, _ = mq.row_groups(ids, L)
+            return mq.lora_add(Y, X, A, B, off, row, scale=scale, out=torch.empty_like(Y))
+
+        step()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = step()
+        runs.append((graph, out, first, second, (Y, X, ids, A, B, scale), torch.cuda.Stream()))
+    for turn in (2, 3, 2):
+        for graph, out, *cs, now, stream in runs:
+            c = cs[turn - 2]
+            for t, k in zip(now, ("Y", "X", "ids", "A", "B", "scale")):
+                t.copy_(c[k])
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for run in runs:
+                with torch.cuda.stream(run[-1]):
+                    run[0].replay()
+        torch.cuda.synchronize()
+        for run in runs:
+            assert torch.equal(run[1], run[turn]["want"])
