@@ -1229,8 +1229,9 @@ constexpr int64_t kLoraBankWork = 8000000;        // many: M / 16 x entries of a
 
 // CTAs of one round: two per SM where their shared memory (static arrays and the system's KB with it) fits twice.
 int64_t lora_room(int32_t r, bool f32, LoraMode mode, int64_t sms) {
-    constexpr int kPerSm = 228 * 1024, kOther = 7 * 1024;
-    return 2 * (lora_smem_bytes(r, lora_padded_rank(r) / 32, f32, mode) + kOther) <= kPerSm ? 2 * sms : sms;
+    constexpr int kPerSm = 228 * 1024;
+    const int other = mode == kFused ? 5888 : 7168;
+    return 2 * (lora_smem_bytes(r, lora_padded_rank(r) / 32, f32, mode) + other) <= kPerSm ? 2 * sms : sms;
 }
 
 // How a call is cut. In 16-row chunks (one launch) A and B are read and multiplied for every 16 rows, in 64-row chunks (two
