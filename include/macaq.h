@@ -310,7 +310,8 @@ macaq_status macaq_moe_w4a16(const void *X, int64_t T, int64_t K, const float *w
  * Low-rank adapters of many requests beside a shared projection:
  *     out[m] = Y[m] + scale[a] * (X[m] A[a]^T) B[a]^T      for the rows m of adapter a
  * with fp32 sums, rounded to out's type. X A^T is held in all of fp32's bits for fp32 outputs and in 16 bits for bf16
- * outputs (off by at most 2^-16 of each of its values), whatever the number of rows.
+ * outputs (off by at most 2^-16 of each of its values), whatever the number of rows. It is added in parts, so that an
+ * infinity in B may come out as NaN; one in X or A does not.
  * Y is the projection's output, from any of the linear calls; X its input (before the activation transform).
  *   Y, out         device [M, N], bf16 or fp32 per dtype (MACAQ_OUT_BF16 / MACAQ_OUT_F32), rows ldy and ldo
  *                  elements apart (>= N): a column slice of a fused projection is fine. out == Y (with
@@ -324,7 +325,8 @@ macaq_status macaq_moe_w4a16(const void *X, int64_t T, int64_t K, const float *w
  *                  gets one of the two results. NULL row_index: the rows are sorted already. Read on the
  *                  device; out-of-range values are clamped or skipped.
  *   workspace      at least macaq_lora_workspace_bytes(M, K, N, r, L, dtype) bytes (0 where one launch does it: may be NULL
- *                  then; K or N of 0: enough for every K or N); no initial value needed, nothing kept between calls. Calls that may overlap need separate ones.
+ *                  then; K or N of 0: enough for every K or N); no initial value needed, nothing kept between calls.
+ *                  Calls that may overlap need separate ones.
  *   K, N, r, ldx, ldy, ldo multiples of 8 (ldy, ldo of fp32: 4); 8 <= r <= 128; 1 <= L <= 1024; M >= 0
  *   (0: no-op), M < 2^31; K, N <= 2^24. Every pointer 16-byte aligned, scale 4-byte.
  */

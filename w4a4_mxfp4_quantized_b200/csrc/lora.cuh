@@ -13,8 +13,10 @@
 // end of a long launch. The first still has a cluster per chunk, each CTA with its share of K: tiles of X and A come
 // through a ring in shared memory, most of a CTA's part at once (4096 wide: 8 tiles, 6 in flight), so that a
 // launch of a few microseconds waits for memory once. It ends with V, in the form the second product takes it, in the
-// workspace (loads straight to the MMAs, a step ahead, took 45.8 us in all for the 2048 rows below). The second takes
+// workspace (loads straight to the MMAs, a step ahead, took 5 us more for the 2048 rows below). The second takes
 // (chunk, slice of the columns) per CTA without clusters and has its first loads of Y and B under way while the first drains.
+// Many adapters, of which few may have rows: grids for every chunk that there could be would mostly be CTAs that find none. There
+// the device counts the chunks and each CTA works out its chunk and slice from that.
 //
 // The other products are bf16 MMAs (m16n8k16) fed straight from global memory: lane (g, t) takes 16 bytes, 8 neighbouring k of
 // row g at 8 t of a 32-wide k step, and the two MMAs of the step take their halves; both operands use the same order, so
@@ -22,10 +24,11 @@
 // ends up with 8 neighbouring columns of a row: Y moves in 16-byte pieces, through a ring of cp.async stages in which each
 // lane reads back what it copied itself (no barrier; the copies of the next steps are in flight while one is added). V is held in
 // two or three bf16 parts (16 or 24 bits).
-// Measured on B200 (4096 -> 14336, a graph that cycles three batches): one row of rank 16 5.4 us; 64 rows over 32 adapters of
-// rank 16 12.4 us (19.7 MB; find 1.0, V 1.9, cluster sum 2.0, columns 5 us); 2048 rows of 4 adapters of rank 64 40.9 us
-// (142 MB, 3.5 TB/s: 10 us for V, most of it starts and the cluster's sum, and 27 us for the columns, whose warps
-// wait on one another's MMAs, shared memory and stores rather than on HBM).
+// Measured on B200 (4096 -> 14336, a graph that cycles three batches): one row of rank 16 5.5 us; 64 rows over 32 adapters of
+// rank 16 12.3 us (19.7 MB; find 1.0, V 1.9, cluster sum 2.0, columns 5 us); 2048 rows of 4 adapters of rank 64 46.4 us
+// (142 MB, 3.1 TB/s: 12 us for V, most of it starts and the cluster's sum, and the rest for the columns, whose warps wait on one
+// another's MMAs, twice as many for V's two parts, shared memory and stores rather than on HBM), of rank 128 80 us, in fp32
+// 89 us. 2048 rows of 4 active adapters of rank 64 in banks of 4, 64, 256 and 1024: 49.8, 50.9, 53.3 and 58.7 us (two batches).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -499,7 +502,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_add_kernel(LoraArgs p) {
         }
         cp_async_commit();   // an empty group keeps groups and steps in step
     };
-    uint4 b[kSteps][4];   // a second set for the next step's, loaded ahead, cost registers and time (50.7 against 45.7 us)
+    uint4 b[kSteps][4];   // a second set for the next step's, loaded ahead, cost registers and time (2048 rows: 5 us)
     auto load_b = [&](int step, uint4 (&to)[kSteps][4]) {
 #pragma unroll
         for (int ks = 0; ks < kSteps; ++ks)
