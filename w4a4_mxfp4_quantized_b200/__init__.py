@@ -467,20 +467,24 @@ def lora_add(Y: torch.Tensor, X: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
     M, N = Y.shape
     L, r, K = A.shape
     out = Y if out is None else out
+    bf16, i32, dtype = torch.bfloat16, torch.int32, _ROWS_DTYPE[Y.dtype]
     yp, ldy = _rows("Y", Y, Y.dtype, M, N, dev)
-    op, ldo = _rows("out", out, Y.dtype, M, N, dev)
-    xp, ldx = _rows("X", X, torch.bfloat16, M, K, dev)
-    bf16, i32 = torch.bfloat16, torch.int32
+    op, ldo = (yp, ldy) if out is Y else _rows("out", out, Y.dtype, M, N, dev)
+    xp, ldx = _rows("X", X, bf16, M, K, dev)
     if workspace is None:   # of this call alone: calls on other streams and captured graphs have their own
-        need = lora_workspace_bytes(M, r, L, _ROWS_DTYPE[Y.dtype], K, N)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
-    _call("macaq_lora_add", dev, yp, ldy, op, ldo, _ROWS_DTYPE[Y.dtype], xp, ldx, M, K, N,
+        need = lora_workspace_bytes(M, r, L, dtype, K, N)
+        if need > 0:
+            workspace = X.new_empty(need // 2)   # of X's two-byte elements: the cheapest allocation from here
+            wp = workspace.data_ptr()
+        else:
+            wp = None
+    else:
+        wp, need = _arg("workspace", workspace, torch.uint8, workspace.shape, dev), workspace.numel()
+    _call("macaq_lora_add", dev, yp, ldy, op, ldo, dtype, xp, ldx, M, K, N,
           _arg("A", A, bf16, (L, r, K), dev), _arg("B", B, bf16, (L, N, r), dev), r, L,
           None if scale is None else _arg("scale", scale, torch.float32, (L,), dev),
           _arg("group_offsets", group_offsets, i32, (L + 1,), dev),
-          None if row_index is None else _arg("row_index", row_index, i32, (M,), dev),
-          None if workspace is None else _arg("workspace", workspace, torch.uint8, workspace.shape, dev),
-          0 if workspace is None else workspace.numel())
+          None if row_index is None else _arg("row_index", row_index, i32, (M,), dev), wp, need)
     return out
 
 

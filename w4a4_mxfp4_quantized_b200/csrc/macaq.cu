@@ -1225,6 +1225,7 @@ macaq_status moe_w4a16(const MoeArgs &a, void *workspace, size_t ws_bytes, cudaS
 // ------------------------------------------------------------------------ low-rank adapters
 constexpr int32_t kLoraManyAdapters = 33;         // from which on the device counts the chunks and shares them out
 constexpr int64_t kLoraColumnWork = 900;          // few adapters: chunks x rank x N / K, from which on two launches are faster
+constexpr int64_t kLoraLeastWork = 4000000;       // few: chunks x entries of A and B, below which it is a microsecond at most
 constexpr int64_t kLoraBankWork = 8000000;        // many: M / 16 x entries of an adapter's A and B, from which on they are
 
 // CTAs of one round: two per SM where their shared memory (static arrays and the system's KB with it) fits twice.
@@ -1244,7 +1245,8 @@ int64_t lora_room(int32_t r, bool f32, LoraMode mode, int64_t sms) {
 // rank 16, 64 rows 7.7 against 8.4, 256 rows 13.4 against 11.1; 4096 -> 4096, rank 64, 64 rows 8.7 against 10.8, 256 rows
 // 13.1 against 11.3; 14336 -> 4096, rank 64, 64 rows 11.8 against 19.3, 512 rows 19.1 against 25.8; 1024 -> 4096, rank 64,
 // 16 rows 7.7 against 7.4. For that ranks up to 32 need 32 rows per adapter (1024 -> 4096, rank 16, 256 rows of 16 adapters
-// 8.0 against 9.7).
+// 8.0 against 9.7). Products so small that there is no more than a microsecond in it stay with one launch, which costs the
+// host 4 us less (from Python 9.7 against 13.5): 16 rows of rank 64 above, 1024 -> 4096, rank 16, 256 rows 7.9 against 6.9.
 // Many adapters, which may mostly have no rows: only the product's size goes into the rule. 4096 -> 14336, rank 16, 256 rows
 // of 4 active adapters 16.9 against 17.5, 512 rows 25.1 against 19.9, of 64 30.7 against 32.1; rank 64, 512 rows of 4 36.9
 // against 24.3, of 64 45.8 against 51.7, of 256 126 against 148; 2048 rows of 4 121 against 51, of 1024 546 against 478;
@@ -1266,7 +1268,8 @@ LoraPlan lora_plan(int64_t M, int32_t L, int32_t r, int64_t K, int64_t N, bool f
     } else {
         const int64_t round = lora_room(r, f32, kFused, kSms) / kLoraCluster * 15 / 16;   // the last clusters find no whole GPC's share
         p.wide = M >= 16 * static_cast<int64_t>(L) &&
-                 (narrow > round || (M >= (r > 32 ? 16 : 32) * static_cast<int64_t>(L) && narrow * r * N > kLoraColumnWork * K));
+                 (narrow > round || (M >= (r > 32 ? 16 : 32) * static_cast<int64_t>(L) && narrow * r * N > kLoraColumnWork * K &&
+                                     narrow * r * (K + N) > kLoraLeastWork));
     }
     p.chunks = p.wide ? lora_chunks(M, L, 64) : narrow;
     return p;
@@ -1613,14 +1616,15 @@ macaq_status macaq_lora_add(const void *Y, int64_t ldy, void *out, int64_t ldo, 
 size_t macaq_lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int32_t r, int32_t L, int32_t dtype) {
     if (M <= 0 || M >= (int64_t(1) << 31) || L < 1 || L > macaq::kRouteMaxExperts || r < 8 || r > macaq::kLoraMaxRank || r % 8)
         return 0;
-    constexpr int64_t kLeast = 8, kMost = int64_t(1) << 24;
+    constexpr int64_t kMost = int64_t(1) << 24;
     if (K < 0 || K > kMost || N < 0 || N > kMost) return 0;
     const bool f32 = dtype == MACAQ_OUT_F32;
-    size_t most = 0;   // a width that is not given may be any: the least and the largest take two launches first, by either rule
-    for (const int64_t k : {K == 0 ? kLeast : K, K == 0 ? kMost : K})
-        for (const int64_t n : {N == 0 ? kLeast : N, N == 0 ? kMost : N})
-            most = std::max(most, macaq::lora_workspace_bytes(macaq::lora_plan(M, L, r, k, n, f32), r, f32));
-    return most;
+    macaq::LoraPlan p = macaq::lora_plan(M, L, r, K, N, f32);
+    if (K == 0 || N == 0) {   // some width may take two launches wherever the rows allow it
+        p.wide = M >= 16 * (L >= macaq::kLoraManyAdapters ? int64_t(1) : L);
+        p.chunks = macaq::lora_chunks(M, L, 64);
+    }
+    return macaq::lora_workspace_bytes(p, r, f32);
 }
 
 }  // extern "C"
